@@ -8,5 +8,6 @@ it to exist:
     from nvfp4_w4a4_expert_amd import build      # compile the library
     from nvfp4_w4a4_expert_amd import _lib       # raw C entry points
     from nvfp4_w4a4_expert_amd import moe        # NVFP4MoELayer + weight prep
+    from nvfp4_w4a4_expert_amd import dense      # norm, 8-bit rows and linear around the experts
 """
-__all__ = ["build", "_lib", "moe"]
+__all__ = ["build", "_lib", "moe", "dense"]

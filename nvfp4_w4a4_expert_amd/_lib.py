@@ -52,6 +52,21 @@ class MoEDebug(ctypes.Structure):
     ]
 
 
+class Linear(ctypes.Structure):
+    _fields_ = [
+        ("a", _p), ("a_scales", _p), ("w", _p), ("w_scales", _p),
+        ("bias", _p), ("residual", _p), ("out", _p), ("out_scales", _p),
+        ("lda", _i64), ("ldw", _i64), ("ldr", _i64), ("ldo", _i64),
+        ("M", _i32), ("N", _i32), ("K", _i32),
+        ("type", _i32), ("bias_type", _i32), ("residual_type", _i32), ("out_type", _i32),
+        ("act", _i32), ("gated", _i32),
+    ]
+
+
+FP8_NONE = -1
+TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_FP8_ROW, TYPE_FP8_MX = range(5)
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
+
 MOE_STAGES = ("route", "permute", "quantize_a1", "gemm1_w13", "gemm2_w2", "combine")
 
 
@@ -82,6 +97,11 @@ _SIGS = {
                                        _p, ctypes.c_size_t, ctypes.POINTER(MoEDebug), _p]),
     "nvfp4_moe_forward_noalloc": (_i32, [ctypes.POINTER(MoEWeights), _p, _p, _i32, _i32, _p, _p,
                                          ctypes.POINTER(MoEDebug), _p]),
+    "nvfp4_rmsnorm": (_i32, [_i32, _p, _i64, _p, _i64, _p, ctypes.c_float, ctypes.c_float, _i32,
+                             _i32, _p, _i64, _p, _i64, _i32, _p, _p, _p]),
+    "nvfp4_quantize_rows_fp8": (_i32, [_i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
+    "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(Linear), ctypes.POINTER(ctypes.c_size_t)]),
+    "nvfp4_linear": (_i32, [ctypes.POINTER(Linear), _p, ctypes.c_size_t, _p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -275,3 +295,29 @@ def moe_forward_noalloc(weights: MoEWeights, x, router_logits, num_tokens: int, 
                                           num_tokens, k, _ptr(residual), _ptr(out),
                                           None if debug is None else ctypes.byref(debug),
                                           _stream(stream)), "nvfp4_moe_forward_noalloc")
+
+
+def rmsnorm(type, x, ldx: int, residual, ldr: int, weight, weight_offset: float, eps: float,
+            num_rows: int, K: int, sum_out, lds: int, y_out, ldy: int, fp8: int, codes, scales,
+            stream=None):
+    _check(_lib.nvfp4_rmsnorm(type, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), weight_offset,
+                              eps, num_rows, K, _ptr(sum_out), lds, _ptr(y_out), ldy, fp8,
+                              _ptr(codes), _ptr(scales), _stream(stream)), "nvfp4_rmsnorm")
+
+
+def quantize_rows_fp8(type, x, ldx: int, num_rows: int, K: int, fp8: int, codes, scales,
+                      stream=None):
+    _check(_lib.nvfp4_quantize_rows_fp8(type, _ptr(x), ldx, num_rows, K, fp8, _ptr(codes),
+                                        _ptr(scales), _stream(stream)), "nvfp4_quantize_rows_fp8")
+
+
+def linear_workspace_size(p: Linear) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.nvfp4_linear_workspace_size(ctypes.byref(p), ctypes.byref(n)),
+           "nvfp4_linear_workspace_size")
+    return n.value
+
+
+def linear(p: Linear, workspace, workspace_bytes: int, stream=None):
+    _check(_lib.nvfp4_linear(ctypes.byref(p), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "nvfp4_linear")

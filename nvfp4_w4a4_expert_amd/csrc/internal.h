@@ -106,4 +106,42 @@ hipError_t launch_combine(const float* c2, const float* w, const int32_t* inv, i
                           int32_t k, int32_t H, const uint16_t* residual, uint16_t* out,
                           hipStream_t stream);
 
+// Row operators of the dense half (rows.hip).  fp8: 0 none, 1 one fp32 scale
+// per row, 2 one UE8M0 scale per 32 elements.
+constexpr int32_t kRowsMaxK = 32768;
+struct RowArgs {
+  const void* x;
+  const void* residual;     // or null (norm only)
+  const void* weight;       // or null (norm only)
+  void* sum_out;            // or null (norm with a residual only)
+  void* y_out;              // or null (norm only)
+  uint8_t* codes;           // null when fp8 == 0
+  void* scales;
+  int64_t ldx, ldr, lds, ldy;
+  int32_t rows, K, fp8;
+  float offset, eps;
+  bool fp16, norm;
+};
+hipError_t launch_rows(const RowArgs& a, hipStream_t stream);
+
+// The dense linear operator (linear.hip).  kind: 0 bf16, 1 fp16, 2 E4M3 with
+// fp32 row scales, 3 E4M3 with UE8M0 block scales.  Element types of bias,
+// residual and out: 0 bf16, 1 fp16, 2 fp32; out also 3: E4M3 with UE8M0 block
+// scales.  act: 0 none, 1 silu, 2 gelu (erf), 3 gelu (tanh form), 4 relu.
+struct LinearArgs {
+  const void* a;            // [M, lda]
+  const void* a_scales;     // fp32 [M] (kind 2) or uint8 [M, K/32] (kind 3)
+  const void* w;            // [N or 2N, ldw]
+  const void* w_scales;
+  const void* bias;         // [N or 2N] or null
+  const void* residual;     // [M, ldr] or null
+  void* out;                // [M, ldo]
+  uint8_t* out_scales;      // [M, N/32] (out type 3)
+  int64_t lda, ldw, ldr, ldo;
+  int32_t M, N, K;
+  int32_t kind, act, gated, bias_type, residual_type, out_type;
+};
+hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream);
+size_t linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t kind, int32_t gated);
+
 }  // namespace nvfp4

@@ -1,0 +1,183 @@
+"""The dense operators around the routed experts, from their formulas (oracle).
+
+TEST INFRASTRUCTURE ONLY (see ``oracle/__init__``).  Values are float64; the
+8-bit row quantiser, whose arithmetic is fixed to single fp32 operations, is
+computed bit for bit.  Each function that a test compares against also gives
+the bound on the fp32 error of the method (u = 2^-24), so tolerances are
+derived here and not fitted.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+
+from . import formats as F
+
+U = 2.0 ** -24
+FLT_MAX = np.finfo(np.float32).max
+
+
+# ---- 8-bit forms ---------------------------------------------------------------
+
+def e4m3_encode(v: np.ndarray) -> np.ndarray:
+    """fp32 -> E4M3 codes: nearest, ties to even, saturating at 448, sign kept;
+    NaN and infinities become the NaN code 0x7F."""
+    v = np.asarray(v, dtype=np.float32)
+    bad = ~np.isfinite(v)
+    mag = F.e4m3_encode(np.where(bad, 0, np.minimum(np.abs(v), np.float32(F.E4M3_MAX))).ravel()).reshape(v.shape)
+    return np.where(bad, 0x7F, mag | np.where(np.signbit(v), 0x80, 0)).astype(np.uint8)
+
+
+def e4m3_decode(c: np.ndarray) -> np.ndarray:
+    m = np.asarray(c).astype(np.int64)
+    mag = F.e4m3_decode_vec(np.minimum(m & 0x7F, 0x7E).astype(np.uint8).ravel()).reshape(m.shape).astype(np.float64)
+    v = np.where(m & 0x80, -mag, mag)
+    return np.where((m & 0x7F) == 0x7F, np.nan, v)
+
+
+def finite_amax(x: np.ndarray, axis) -> np.ndarray:
+    return np.where(np.isfinite(x), np.abs(x), 0).max(axis=axis, initial=0)
+
+
+def quantize_row(x: np.ndarray):
+    """fp32 rows -> (codes, fp32 scale per row), one fp32 operation at a time."""
+    x = np.asarray(x, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        s = (finite_amax(x, 1).astype(np.float32) / np.float32(448)).astype(np.float32)
+        inv = np.where(s > 0, np.minimum(np.float32(1) / s, np.float32(FLT_MAX)), np.float32(0)).astype(np.float32)
+        v = (x * inv[:, None]).astype(np.float32)
+    return e4m3_encode(np.where(np.isfinite(x), v, np.nan)), s
+
+
+def block_code(amax: np.ndarray) -> np.ndarray:
+    """UE8M0 code of the smallest power of two P with amax <= 448 P."""
+    m, e = np.frexp(np.asarray(amax, dtype=np.float64))         # amax = m 2^e, 448 = 0.875 * 2^9
+    p = e - 9 + (m > 0.875)
+    return np.clip(np.where(m > 0, p, -127) + 127, 1, 254).astype(np.uint8)
+
+
+def quantize_block(x: np.ndarray):
+    """fp32 rows -> (codes, UE8M0 code per 32 elements)."""
+    x = np.asarray(x, dtype=np.float32)
+    b = x.reshape(x.shape[0], -1, 32)
+    c = block_code(finite_amax(b, 2))
+    with np.errstate(all="ignore"):
+        v = np.ldexp(b, (127 - c.astype(np.int32))[..., None]).astype(np.float32)
+    return e4m3_encode(np.where(np.isfinite(b), v, np.nan)).reshape(x.shape), c
+
+
+def scale_values(scales: np.ndarray, K: int) -> np.ndarray:
+    """Scales of either form, one per element, in float64."""
+    if scales.dtype == np.uint8:
+        return np.repeat(2.0 ** (scales.astype(np.float64) - 127), 32, axis=1)
+    return np.repeat(scales.astype(np.float64)[:, None], K, axis=1)
+
+
+def dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    return e4m3_decode(codes) * scale_values(scales, codes.shape[1])
+
+
+def check_fp8(codes, scales, y, err, label=""):
+    """codes / scales hold float64 values y known to the kernel up to `err`: the
+    scale belongs to an amax within err, and each code is the E4M3 number
+    nearest to a value within err of y / scale.  E4M3's half step is 2^-4 of the
+    value, at least 2^-10 (subnormals are multiples of 2^-9)."""
+    K = y.shape[1]
+    err = np.broadcast_to(err, y.shape)
+    if scales.dtype == np.uint8:
+        b, be = np.abs(y).reshape(y.shape[0], -1, 32), err.reshape(y.shape[0], -1, 32)
+        lo, hi = block_code((b - be).clip(0).max(2)), block_code((b + be).max(2))
+        assert np.all((scales >= lo) & (scales <= hi)), f"{label}: block scale"
+        s_err = 0.0
+    else:
+        hi, lo = (np.abs(y) + err).max(1) / 448, (np.abs(y) - err).clip(0).max(1) / 448
+        s = scales.astype(np.float64)
+        assert np.all((s <= hi * (1 + 2 * U) + 2.0 ** -149) & (s >= lo * (1 - 2 * U) - 2.0 ** -149)), f"{label}: row scale"
+        s_err = 4 * U                                       # 1 / scale, the product, the saturation at a rounded scale
+    sv = scale_values(scales, K)
+    got = e4m3_decode(codes) * sv
+    mag = np.abs(y) + err
+    tol = np.maximum(mag * 2.0 ** -4, sv * 2.0 ** -10) * (1 + 2.0 ** -20) + err + s_err * mag
+    # a row or block without a nonzero element has scale 0 (row) or codes 0
+    off = np.abs(got - y) - tol
+    assert np.all(off <= 0), f"{label}: code off by {off.max():.3g} over its bound"
+
+
+# ---- norm ----------------------------------------------------------------------
+
+def rms_norm(s, weight, eps, offset):
+    """(y, fp32 error bound) of rows s: the sum of K squares is added in runs of
+    at most 32 per thread, 6 levels in a wavefront and 16 wavefronts (relative
+    error 56 u of a sum of positive terms), halved by the root; quotient, sum,
+    root, reciprocal, offset and two products add 8 u."""
+    s = np.asarray(s, dtype=np.float64)
+    g = 1.0 if weight is None else offset + np.asarray(weight, dtype=np.float64)
+    y = s / np.sqrt((s * s).mean(axis=1, keepdims=True) + eps) * g
+    return y, np.abs(y) * 36 * U + 2.0 ** -148
+
+
+# ---- linear --------------------------------------------------------------------
+
+def activate(v, act):
+    with np.errstate(over="ignore"):
+        if act == "silu":
+            return v / (1 + np.exp(-v))
+        if act == "gelu":
+            from math import erfc
+            return v * np.vectorize(erfc, otypes=[np.float64])(-v / math.sqrt(2)) / 2
+        if act == "gelu_tanh":
+            # (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which does not cancel for negative u
+            return v / (1 + np.exp(-2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+        return np.maximum(v, 0) if act == "relu" else v
+
+
+def linear(a, w, bias=None, act=None, gated=False, residual=None, scaled=False):
+    """(out, fp32 error bound), all float64.  Sums: one rounding per step of a
+    32-deep matrix instruction and a budget of 64 for the instruction's own sum
+    and the scales' products, relative to sum |a w|; |act'| <= 1.2 for every
+    activation (gelu's slope peaks at 1.13); its evaluation is off by at most
+    (16 + 4 |v|) u of its value plus 16 u |v| for erfc's fit (fractional 1.2e-7
+    and the rounded argument of exp); product, residual: one rounding each.
+
+    scaled: 8-bit operands on the scaled matrix instruction, which cuts each
+    product to a multiple of 2^-13 of the largest power of two among its group
+    of eight (towards zero).  The cut of product i is uniform in [0, 2^-13 max]
+    with the product's sign: for random signs the sum's deviation is at most
+    2^-13 / sqrt(3) * sqrt(8 sum p^2), and eight of them 2^-9.3 sqrt(sum p^2)."""
+    K = a.shape[1]
+    v = a @ w.T
+    e = (K / 32 + 64) * U * (np.abs(a) @ np.abs(w).T)
+    if scaled:
+        e = e + 2.0 ** -9.3 * np.sqrt((a * a) @ (w * w).T)
+    if bias is not None:
+        v = v + bias
+        e = e + U * np.abs(v)
+    N = w.shape[0] // 2 if gated else w.shape[0]
+    g, ge = v[:, :N], e[:, :N]
+    out = activate(g, act)
+    err = 1.2 * ge
+    if act not in (None, "none", "relu"):
+        err = err + (16 + 4 * np.abs(g)) * U * np.abs(out) + 16 * U * np.abs(g)
+    if gated:
+        u, ue = v[:, N:], e[:, N:]
+        err = np.abs(u) * err + np.abs(out) * ue + err * ue
+        out = out * u
+        err = err + U * np.abs(out)
+    if residual is not None:
+        out = out + residual
+        err = err + U * np.abs(out)
+    return out, err
+
+
+HALF_STEP = {"bfloat16": 2.0 ** -8, "float16": 2.0 ** -11, "float32": 2.0 ** -24}
+SUBNORMAL = {"bfloat16": 2.0 ** -134, "float16": 2.0 ** -25, "float32": 2.0 ** -150}
+
+
+def check_rounded(got, ref, err, dtype, label=""):
+    """got (float64 values of a `dtype` tensor) is ref, known up to err, rounded
+    once: off by at most half a step of the type."""
+    d = str(dtype).replace("torch.", "")
+    tol = (np.abs(ref) + err) * HALF_STEP[d] + SUBNORMAL[d] + err
+    off = np.abs(got - ref) - tol
+    assert np.all(off <= 0), f"{label}: off by {off.max():.3g} over its bound"
