@@ -58,9 +58,6 @@ struct LinParams {
   int32_t tiles_m, tiles_n;
 };
 
-// 16 zero bytes: the source of a chunk past the end of a row.
-__device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
-
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int32_t type) {
   if (type == kOutF32) return static_cast<const float*>(p)[i];
   const uint16_t u = static_cast<const uint16_t*>(p)[i];
@@ -234,6 +231,33 @@ __device__ __forceinline__ void store_run(const LinParams& p, int64_t m, int32_t
   }
 }
 
+// kLen consecutive outputs as E4M3 codes; 32 / kLen neighbouring lanes hold a block
+// of 32 columns (N is a multiple of 32: a block is stored whole or not at all)
+// and agree on its scale.
+template <int kLen>
+__device__ __forceinline__ void store_block(const LinParams& p, int64_t m, int32_t n, const float* v, bool in) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kLen; ++i) top = max(top, finite_mag(v[i]));
+#pragma unroll
+  for (int off = 1; off < 32 / kLen; off *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+  float inv;
+  const uint32_t code = block_scale_code(top, inv);
+  if (!in) return;
+  uint8_t* dst = static_cast<uint8_t*>(p.out) + m * p.ldo + n;
+#pragma unroll
+  for (int i = 0; i < kLen; i += 4) *reinterpret_cast<uint32_t*>(dst + i) = encode4_e4m3(v + i, inv);
+  if (n % 32 == 0) p.out_scales[m * (p.N / 32) + n / 32] = (uint8_t)code;
+}
+
+// Workgroup barrier that orders LDS accesses only: stores to memory need not
+// have completed, as a full __syncthreads() would demand.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // A lane's share of a K step of one row of 16: the 16-byte chunks g and 4 + g of
 // the 128 bytes, g its group of 16 lanes.  That is the K order of the
 // 16x16x128 instruction, whose lane group g also supplies the scale of the
@@ -253,35 +277,40 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale
   return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// An operand's share as the instruction takes it, and its scale.
-template <int kKind>
+// An operand's share as the instruction takes it.  Block scales: a row's UE8M0
+// codes of four steps lie in one word per block of a step, step t in byte t; a
+// lane holds the word of the g-th block, or (wide kinds) those of the blocks of
+// chunks g and 4 + g.
+constexpr uint32_t kUnit = 0x7F7F7F7Fu;                           // scale 1 in every byte
+
+template <int kKind, int kByte>
 struct Prepared {
   Frag f;
   uint32_t scale;
-  __device__ __forceinline__ void set(const Frag& v, uint32_t s) { f = v; scale = s; }
+  __device__ __forceinline__ void set(const Frag& v, const uint32_t* s) { f = v; scale = s[0]; }
 };
+template <int kByte>
 struct PreparedWide {
   bf16x8_t v[4];
-  // s: UE8M0 codes of chunk g's and chunk 4 + g's blocks in the low two bytes
-  __device__ __forceinline__ void set(const Frag& f, uint32_t s) {
+  __device__ __forceinline__ void set(const Frag& f, const uint32_t* s) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const uint32_t e = (s >> (8 * c)) & 0xFFu;
-      const float scale = __uint_as_float(e << 23);               // 2^(code - 127), code in [1, 254]
+      // 2^(code - 127), code in [1, 254]
+      const float scale = __uint_as_float(((s[c] >> (8 * kByte)) & 0xFFu) << 23);
       v[2 * c] = widen8(f.c[c].x, f.c[c].y, scale);
       v[2 * c + 1] = widen8(f.c[c].z, f.c[c].w, scale);
     }
   }
 };
-template <>
-struct Prepared<kRow8Wide> : PreparedWide {};
-template <>
-struct Prepared<kBlock8Wide> : PreparedWide {};
+template <int kByte>
+struct Prepared<kRow8Wide, kByte> : PreparedWide<kByte> {};
+template <int kByte>
+struct Prepared<kBlock8Wide, kByte> : PreparedWide<kByte> {};
 
 // acc += w . a over a K step; w is the row operand, so a lane's four results are
 // four consecutive output columns (instruction rows 4g .. 4g + 3) of one row of a.
-template <int kKind>
-__device__ __forceinline__ f32x4 mma(const Prepared<kKind>& w, const Prepared<kKind>& a, f32x4 acc) {
+template <int kKind, int kByte>
+__device__ __forceinline__ f32x4 mma(const Prepared<kKind, kByte>& w, const Prepared<kKind, kByte>& a, f32x4 acc) {
   if constexpr (is_wide(kKind)) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[t], a.v[t], acc, 0, 0, 0);
@@ -297,20 +326,32 @@ __device__ __forceinline__ f32x4 mma(const Prepared<kKind>& w, const Prepared<kK
                                                    __builtin_bit_cast(half8_t, a.f.c[t]), acc, 0, 0, 0);
   } else {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8_t, w.f), __builtin_bit_cast(i32x8_t, a.f),
-                                                           acc, 0, 0, 0, (int)w.scale, 0, (int)a.scale);
+                                                           acc, 0, 0, kByte, (int)w.scale, kByte, (int)a.scale);
   }
   return acc;
 }
 
-// The scale operand of a lane for K step `ks` of a row whose block scales are
-// `row` (nblk of them): group g's block of the step, or the blocks of chunks g
-// and 4 + g for the wide kind.  Past the end the data are zeros: any scale does.
-template <int kKind>
-__device__ __forceinline__ uint32_t step_scale(const uint8_t* row, int ks, int g, int nblk) {
-  if constexpr (kKind == kBlock8) return row[min(4 * ks + g, nblk - 1)];
-  if constexpr (kKind == kBlock8Wide)
-    return row[min(4 * ks + g / 2, nblk - 1)] | ((uint32_t)row[min(4 * ks + 2 + g / 2, nblk - 1)] << 8);
-  return 0x7F7Fu;
+// 16 scales of a row, of the four steps from block `at` on, as four words, one per
+// block of a step (byte t: step t).  Past the end of the row the data are zeros:
+// any scale does.
+__device__ __forceinline__ u32x4 load_scales(const uint8_t* row, int at, int nblk) {
+  u32x4 d;
+  if (at + 16 <= nblk) {
+    __builtin_memcpy(&d, row + at, 16);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w |= (at + 4 * t + b < nblk ? (uint32_t)row[at + 4 * t + b] : 127u) << (8 * b);
+      d[t] = w;
+    }
+  }
+  // 4 x 4 bytes transposed
+  const uint32_t lo01 = __builtin_amdgcn_perm(d.y, d.x, 0x05010400u), hi01 = __builtin_amdgcn_perm(d.y, d.x, 0x07030602u);
+  const uint32_t lo23 = __builtin_amdgcn_perm(d.w, d.z, 0x05010400u), hi23 = __builtin_amdgcn_perm(d.w, d.z, 0x07030602u);
+  return u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100u), __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
+               __builtin_amdgcn_perm(hi23, hi01, 0x05040100u), __builtin_amdgcn_perm(hi23, hi01, 0x07060302u)};
 }
 
 // A lane's share from a 128-byte row segment in LDS whose chunk c lies at
@@ -329,24 +370,35 @@ __device__ __forceinline__ void load_lds16(const char* src, char* lds) {
                                    (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
+// Barrier at the turn of a step: this wavefront's copies into LDS have arrived
+// and its LDS reads are done before any wavefront passes.  The wait is written
+// out because the copies are counted with memory loads, whose completion a
+// workgroup barrier by itself does not ask for.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  lds_barrier();
+}
+
 // ---- tiled kernel -------------------------------------------------------------
 // A workgroup of kWM x kWN wavefronts owns kBM rows of a and kBN rows of w
-// (gated: kBN / 2 output columns, their gate and their up rows).  Each K step's
-// rows are copied straight into LDS (two buffers); the rows of w are placed so
-// that the four results of each of a wavefront's instructions continue each
-// other: a lane ends with kRun consecutive outputs of each of its rows.
+// (gated: kBN / 2 output columns, their gate rows, then their up rows).  Each K
+// step's rows are copied straight into LDS (two buffers).  The epilogue passes
+// the sums through LDS, 32 rows of each wavefront at a time, so that every thread
+// finishes 8 consecutive outputs of a row and whole rows are stored.
 template <int kKind, int kBM, int kBN, int kWM, int kWN, bool kGated>
 __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinParams p) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kTM = kBM / kWM, kTN = kBN / kWN;
   constexpr int kFM = kTM / 16, kFN = kTN / 16;
-  constexpr int kGF = kGated ? kFN / 2 : kFN;                  // instructions per output column group
-  constexpr int kRun = 4 * kGF;                                // consecutive outputs of a lane
   constexpr int kOutN = kGated ? kBN / 2 : kBN;                // output columns of the tile
   constexpr int kStage = (kBM + kBN) * kStep;
   constexpr int kLoads = (kBM + kBN) / 8 / kWaves;             // 1 KiB copies per wavefront and step
   static_assert((kBM + kBN) / 8 % kWaves == 0 && kBM / 8 % kLoads == 0, "whole copies; a wavefront copies one operand");
+  static_assert(!kGated || kOutN % (8 * kLoads) == 0 || 8 * kLoads % kOutN == 0, "a copy holds gate or up rows");
+  constexpr bool kScaled = is_block8(kKind);
+  static_assert(kBM + kBN == 64 * kWaves || !kScaled, "a thread loads the scales of one row");
   __shared__ __align__(1024) char smem[2 * kStage];
+  __shared__ __align__(16) uint32_t s_scale[kScaled ? 2 : 1][kScaled ? kBM + kBN : 1][4];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
@@ -370,36 +422,42 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
   const int64_t m0 = (int64_t)tm * kBM;
   const int32_t n0 = tn * kOutN;
 
-  // source of each copy: lane -> (row of the tile, chunk); rows past the edge
-  // repeat the last row, their results are not stored
-  const char* src[kLoads];
+  // source of each copy: lane -> (row of the tile, chunk), as an offset from the
+  // tile's first row; rows past the edge repeat the last row, their results are
+  // not stored
+  uint32_t off[kLoads];
+  uint64_t src[kLoads];                                        // uniform: the operand's tile (and half) at this step
   const int chunk = (lane & 7) ^ (lane >> 3);                  // (row & 7) == lane >> 3
   const bool is_a = wave * kLoads * 8 < kBM;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int r = (wave * kLoads + i) * 8 + (lane >> 3);
     if (is_a) {
-      const int64_t m = m0 + r;
-      src[i] = p.a + (m < p.M ? m : (int64_t)p.M - 1) * p.lda + chunk * 16;
+      const int32_t last = (int32_t)min((int64_t)kBM, p.M - m0) - 1;
+      src[i] = reinterpret_cast<uint64_t>(p.a + m0 * p.lda);
+      off[i] = (uint32_t)(r < last ? r : last) * (uint32_t)p.lda + chunk * 16;
     } else {
-      const int q = (r - kBM) % kTN, f = q / 16, x = q % 16;
-      int32_t n = n0 + (r - kBM) / kTN * (kOutN / kWN) + (x / 4) * kRun + (f % kGF) * 4 + x % 4;
-      n = n < p.N ? n : p.N - 1;
-      src[i] = p.w + ((int64_t)n + (f >= kGF ? p.N : 0)) * p.ldw + chunk * 16;
+      const int c = (r - kBM) % kOutN, last = min(kOutN, p.N - n0) - 1;
+      const bool up = (wave * kLoads + i) * 8 - kBM >= kOutN;      // the same for the copy's 8 rows
+      src[i] = reinterpret_cast<uint64_t>(p.w + ((int64_t)n0 + (up ? p.N : 0)) * p.ldw);
+      off[i] = (uint32_t)(c < last ? c : last) * (uint32_t)p.ldw + chunk * 16;
     }
   }
   const int steps = (p.kbytes + kStep - 1) / kStep;
   const int tail = p.kbytes - (steps - 1) * kStep;             // bytes of the last step
   auto fetch = [&](int ks) {
     char* dst = smem + (ks & 1) * kStage + wave * kLoads * 1024;
-    if (ks == steps - 1 && chunk * 16 >= tail) {
+    if (chunk * 16 < (ks == steps - 1 ? tail : kStep)) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) src[i] = reinterpret_cast<const char*>(g_zeros);
+      for (int i = 0; i < kLoads; ++i) load_lds16(reinterpret_cast<const char*>(src[i]) + off[i], dst + i * 1024);
+    } else {                                                   // past the end of the rows
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(dst + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      load_lds16(src[i], dst + i * 1024);
       src[i] += kStep;
+      asm volatile("" : "+s"(src[i]));                         // kept in scalar registers, apart from the lanes' offsets
     }
   };
 
@@ -409,85 +467,158 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
 #pragma unroll
     for (int i = 0; i < kFM; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
 
-  // block scales: this lane's byte of each fragment's four blocks of a step
-  const uint8_t* sa[is_block8(kKind) ? kFM : 1] = {};
-  const uint8_t* sw[is_block8(kKind) ? kFN : 1] = {};
+  // block scales: every thread loads those of one row of the tile, four steps at
+  // a time, and leaves them in LDS
   const int32_t nblk = p.kbytes / 32;
-  if constexpr (is_block8(kKind)) {
-#pragma unroll
-    for (int i = 0; i < kFM; ++i) {
-      const int64_t m = m0 + wm * kTM + i * 16 + i16;
-      sa[i] = static_cast<const uint8_t*>(p.a_scales) + (m < p.M ? m : (int64_t)p.M - 1) * nblk;
+  const uint8_t* scale_row = nullptr;
+  u32x4 scale_next;
+  if constexpr (kScaled) {
+    const int r = threadIdx.x;
+    if (r < kBM) {
+      scale_row = static_cast<const uint8_t*>(p.a_scales) + min(m0 + r, (int64_t)p.M - 1) * nblk;
+    } else {
+      const int q = r - kBM;
+      scale_row = static_cast<const uint8_t*>(p.w_scales) +
+                  ((int64_t)min(n0 + q % kOutN, p.N - 1) + (q >= kOutN ? p.N : 0)) * nblk;
     }
+  }
+
+  // Main loop.  A step runs its groups of instructions (one 16-row fragment of a
+  // with all of w) in order, the fragments of a being read two groups ahead; the
+  // last two groups run fragment of w by fragment of w.  The barrier falls before
+  // them: behind it the buffer that the step has read is refilled for the step
+  // after next, and each fragment of w is replaced by the next step's as soon as
+  // its last instruction is issued, so the matrix unit does not wait for LDS at
+  // the turn of a step.  The scheduling barriers keep the compiler from moving
+  // the reads back to their uses.  T: the step's number modulo 4 (2 without block
+  // scales), for the byte of the scales and the slots of fa when a step has only
+  // two groups.
+  static_assert(kFM == 2 || kFM % 4 == 0, "fragment slots");
+  constexpr int kUnroll = kScaled ? 4 : 2;
+  constexpr int kWords = kKind == kBlock8Wide ? 2 : 1;         // scale words of a lane and row
+  Frag fa[4], fw[kFN];
+  uint32_t va[kFM][2], vw[kFN][2];
+#pragma unroll
+  for (int i = 0; i < kFM; ++i) va[i][0] = va[i][1] = kUnit;
+#pragma unroll
+  for (int j = 0; j < kFN; ++j) vw[j][0] = vw[j][1] = kUnit;
+  auto read_scales = [&](int buf) {
+#pragma unroll
+    for (int c = 0; c < kWords; ++c) {
+      const int word = kKind == kBlock8Wide ? 2 * c + g / 2 : g;
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) va[i][c] = s_scale[kScaled ? buf : 0][kScaled ? wm * kTM + i * 16 + i16 : 0][word];
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) vw[j][c] = s_scale[kScaled ? buf : 0][kScaled ? kBM + wn * kTN + j * 16 + i16 : 0][word];
+    }
+  };
+  auto step = [&](auto t, int ks) {
+    constexpr int T = decltype(t)::value;
+    constexpr int kBase = kFM == 2 ? 2 * (T & 1) : 0;          // slot of group 0
+    constexpr int kNext = kFM == 2 ? 2 - 2 * (T & 1) : 0;      // slot of the next step's group 0
+    typedef Prepared<kKind, T> Op;
+    const char* ta = smem + (ks & 1) * kStage + wm * kTM * kStep;
+    const char* na = smem + (1 - (ks & 1)) * kStage + wm * kTM * kStep;
+    const char* nw = smem + (1 - (ks & 1)) * kStage + (kBM + wn * kTN) * kStep;
+    if constexpr (kScaled && T == 0) read_scales((ks >> 2) & 1);
+    Op pw[kFN];
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) pw[j].set(fw[j], vw[j]);
+#pragma unroll
+    for (int i = 0; i < kFM - 2; ++i) {
+      fa[(kBase + i + 2) & 3] = read_frag(ta, (i + 2) * 16 + i16, g);
+      __builtin_amdgcn_sched_barrier(0);
+      Op pa;
+      pa.set(fa[(kBase + i) & 3], va[i]);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) acc[j][i] = mma<kKind, T>(pw[j], pa, acc[j][i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kScaled) {
+      // the next four steps' scales: loaded a step before they go to LDS, which
+      // is a step before they are read
+      if constexpr (T == 1) scale_next = load_scales(scale_row, 4 * (ks + 3), nblk);
+      if constexpr (T == 2) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_next;
+    }
+    step_barrier();                                            // this buffer is read, the other one filled
+    if (ks + 2 < steps) fetch(ks + 2);
+    Op pa[2];
+    pa[0].set(fa[(kBase + kFM - 2) & 3], va[kFM - 2]);
+    pa[1].set(fa[(kBase + kFM - 1) & 3], va[kFM - 1]);
+    // (after the last step these read an older one, unused)
+    fa[kNext] = read_frag(na, i16, g);
+    fa[kNext + 1] = read_frag(na, 16 + i16, g);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
-      int32_t n = n0 + wn * (kOutN / kWN) + (i16 / 4) * kRun + (j % kGF) * 4 + i16 % 4;
-      n = n < p.N ? n : p.N - 1;
-      sw[j] = static_cast<const uint8_t*>(p.w_scales) + ((int64_t)n + (j >= kGF ? p.N : 0)) * nblk;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[j][kFM - 2 + i] = mma<kKind, T>(pw[j], pa[i], acc[j][kFM - 2 + i]);
+      fw[j] = read_frag(nw, j * 16 + i16, g);
+      __builtin_amdgcn_sched_barrier(0);
     }
-  }
-
+  };
   fetch(0);
-  for (int ks = 0; ks < steps; ++ks) {
-    __syncthreads();                                           // this step's rows are in LDS; the other buffer is free
-    if (ks + 1 < steps) fetch(ks + 1);
-    const char* ta = smem + (ks & 1) * kStage + wm * kTM * kStep;
-    const char* tw = smem + (ks & 1) * kStage + (kBM + wn * kTN) * kStep;
-    uint32_t va[kFM], vw[kFN];
+  if (steps > 1) fetch(1);
+  if constexpr (kScaled) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = load_scales(scale_row, 0, nblk);
+  step_barrier();
 #pragma unroll
-    for (int i = 0; i < kFM; ++i) va[i] = step_scale<kKind>(sa[is_block8(kKind) ? i : 0], ks, g, nblk);
-#pragma unroll
-    for (int j = 0; j < kFN; ++j) vw[j] = step_scale<kKind>(sw[is_block8(kKind) ? j : 0], ks, g, nblk);
-    Prepared<kKind> fw[kFN];
-#pragma unroll
-    for (int j = 0; j < kFN; ++j) fw[j].set(read_frag(tw, j * 16 + i16, g), vw[j]);
-#pragma unroll
-    for (int i = 0; i < kFM; ++i) {
-      Prepared<kKind> fa;
-      fa.set(read_frag(ta, i * 16 + i16, g), va[i]);
-#pragma unroll
-      for (int j = 0; j < kFN; ++j) acc[j][i] = mma<kKind>(fw[j], fa, acc[j][i]);
+  for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + (kBM + wn * kTN) * kStep, j * 16 + i16, g);
+  fa[0] = read_frag(smem + wm * kTM * kStep, i16, g);
+  fa[1] = read_frag(smem + wm * kTM * kStep, 16 + i16, g);
+  for (int ks = 0; ks < steps; ks += kUnroll) {
+    step(std::integral_constant<int, 0>{}, ks);
+    if (ks + 1 < steps) step(std::integral_constant<int, 1>{}, ks + 1);
+    if constexpr (kUnroll == 4) {
+      if (ks + 2 < steps) step(std::integral_constant<int, 2>{}, ks + 2);
+      if (ks + 3 < steps) step(std::integral_constant<int, 3>{}, ks + 3);
     }
   }
 
-  const int32_t n = n0 + wn * (kOutN / kWN) + g * kRun;
-  Columns<kKind, kGated, kRun> cols;
+  // Epilogue: groups 2 * pass and 2 * pass + 1 of every wavefront through LDS.
+  constexpr int kLd = kBN + 4;                                 // floats per row: 8 rows start on distinct banks
+  constexpr int kRows = 32 * kWM;
+  constexpr int kPer = kOutN / 8;                              // threads per row
+  static_assert(kRows * kLd * 4 <= 2 * kStage, "the pass fits the step buffers");
+  float* tile = reinterpret_cast<float*>(smem);
+  const int c = (int)(threadIdx.x % kPer) * 8;
+  const int32_t n = n0 + c;
+  Columns<kKind, kGated, 8> cols;
   cols.load(p, n);
+#pragma unroll 1
+  for (int pass = 0; pass < kFM / 2; ++pass) {
+    lds_barrier();                                             // the steps' (or the last pass's) reads are done
+    float* dst = tile + (wm * 32 + i16) * kLd + wn * kTN + 4 * g;
 #pragma unroll
-  for (int i = 0; i < kFM; ++i) {
-    const int64_t m = m0 + wm * kTM + i * 16 + i16;
-    float v[kRun], u[kRun];
+    for (int q = 0; q < kFM / 2; ++q)
+      if (q == pass) {
 #pragma unroll
-    for (int j = 0; j < kGF; ++j)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[4 * j + r] = acc[j][i][r];
-        u[4 * j + r] = kGated ? acc[j + (kGated ? kGF : 0)][i][r] : 0.0f;
+          for (int j = 0; j < kFN; ++j) *reinterpret_cast<f32x4*>(dst + i * 16 * kLd + j * 16) = acc[j][2 * q + i];
       }
-    const bool in = m < p.M;
-    const int64_t mr = in ? m : (int64_t)p.M - 1;
-    cols.finish(p, mr, v, u);
-    add_residual<kRun>(p, mr, n, v);
-    if (p.out_type != kOutBlock8) {
-      if (in) store_run<kRun>(p, m, n, v);
-    } else if constexpr (4 * kRun >= 32) {
-      // a block of 32 columns lies in 32 / kRun neighbouring lane groups; N is a
-      // multiple of 32, so it is stored whole or not at all
-      uint32_t top = 0;
+    lds_barrier();
+#pragma unroll 1
+    for (int r = (int)threadIdx.x / kPer; r < kRows; r += 64 * kWaves / kPer) {
+      const int64_t m = m0 + (r / 32) * kTM + pass * 32 + r % 32;
+      const bool in = m < p.M && n < p.N;
+      const int64_t mr = m < p.M ? m : (int64_t)p.M - 1;
+      float v[8], u[8];
 #pragma unroll
-      for (int c = 0; c < kRun; ++c) top = max(top, finite_mag(v[c]));
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(tile + r * kLd + c + 4 * h);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(tile + r * kLd + c + 4 * h + (kGated ? kOutN : 0));
 #pragma unroll
-      for (int off = 16; off < 16 * (32 / kRun); off *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-      float inv;
-      const uint32_t code = block_scale_code(top, inv);
-      if (in && n < p.N) {
-        uint32_t d[kRun / 4];
-#pragma unroll
-        for (int c = 0; c < kRun / 4; ++c) d[c] = encode4_e4m3(v + 4 * c, inv);
-        uint8_t* dst = static_cast<uint8_t*>(p.out) + m * p.ldo + n;
-#pragma unroll
-        for (int c = 0; c < kRun / 4; c += 2) *reinterpret_cast<uint2*>(dst + 4 * c) = uint2{d[c], d[c + 1]};
-        if (n % 32 == 0) p.out_scales[m * (p.N / 32) + n / 32] = (uint8_t)code;
+        for (int e = 0; e < 4; ++e) {
+          v[4 * h + e] = x[e];
+          u[4 * h + e] = y[e];
+        }
+      }
+      cols.finish(p, mr, v, u);
+      add_residual<8>(p, mr, n, v);
+      if (p.out_type != kOutBlock8) {
+        if (in) store_run<8>(p, m, n, v);
+      } else {
+        store_block<8>(p, m, n, v, in);
       }
     }
   }
@@ -555,15 +686,31 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
         if (in) fa[i].c[c] = *reinterpret_cast<const u32x4*>(pa[i] + at);
       }
     }
-    Prepared<kKind> qw[kFN], qa[kFM];
+    // this step's scales of the blocks of chunks g and 4 + g (past the end the
+    // data are zeros: any scale does)
+    auto scales = [&](const uint8_t* row, uint32_t* d) {
+      d[0] = d[1] = kUnit;
+      if constexpr (is_block8(kKind)) {
+        d[0] = row[min(4 * ks + g / 2, nblk - 1)];
+        d[1] = row[min(4 * ks + 2 + g / 2, nblk - 1)];
+      }
+    };
+    Prepared<kKind, 0> qw[kFN], qa[kFM];
+    uint32_t sc[2];
 #pragma unroll
-    for (int j = 0; j < kFN; ++j) qw[j].set(fw[j], step_scale<kKind>(sw[j], ks, g, nblk));
+    for (int j = 0; j < kFN; ++j) {
+      scales(sw[j], sc);
+      qw[j].set(fw[j], sc);
+    }
 #pragma unroll
-    for (int i = 0; i < kFM; ++i) qa[i].set(fa[i], step_scale<kKind>(sa[i], ks, g, nblk));
+    for (int i = 0; i < kFM; ++i) {
+      scales(sa[i], sc);
+      qa[i].set(fa[i], sc);
+    }
 #pragma unroll
     for (int j = 0; j < kFN; ++j)
 #pragma unroll
-      for (int i = 0; i < kFM; ++i) acc[j][i] = mma<kKind>(qw[j], qa[i], acc[j][i]);
+      for (int i = 0; i < kFM; ++i) acc[j][i] = mma<kKind, 0>(qw[j], qa[i], acc[j][i]);
   }
 #pragma unroll
   for (int j = 0; j < kFN; ++j)
@@ -595,17 +742,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
     if (p.out_type != kOutBlock8) {
       if (in) store_run<4>(p, m, n, gv);
     } else if constexpr (kCols % 32 == 0) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, finite_mag(gv[i]));
-#pragma unroll
-      for (int off = 1; off < 8; off *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-      float inv;
-      const uint32_t code = block_scale_code(top, inv);
-      if (in) {
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + m * p.ldo + n) = encode4_e4m3(gv, inv);
-        if (n % 32 == 0) p.out_scales[m * (p.N / 32) + n / 32] = (uint8_t)code;
-      }
+      store_block<4>(p, m, n, gv, in);
     }
   }
 }
@@ -642,7 +779,7 @@ hipError_t go(const LinParams& p, hipStream_t stream) {
     }
   }
   if constexpr (kKind == kRow8 || kKind == kBlock8)
-    if (p.out_type == kOutF32) return go<kKind == kRow8 ? kRow8Wide : kBlock8Wide, kGated>(p, stream);
+    if (p.out_type == kOutF32 || p.out_type == kOutBlock8) return go<kKind == kRow8 ? kRow8Wide : kBlock8Wide, kGated>(p, stream);
   const int64_t cols = kGated ? 2 * (int64_t)p.N : p.N;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm) * ((cols + bn - 1) / bn); };
   if constexpr (!is_wide(kKind))

@@ -19,8 +19,7 @@ graph.  Forward only: no gradients are recorded.
 """
 from __future__ import annotations
 
-import ctypes
-import operator
+import contextlib
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -57,33 +56,32 @@ class NormOut(NamedTuple):
     fp8: Optional[FP8Rows]
 
 
+_HALF = (torch.bfloat16, torch.float16)
+_BYTES = (torch.uint8,)
+_FLOATS = tuple(_TYPES)
+
+
 def _need(ok, msg):
     if not ok:
         raise ValueError(msg)
 
 
-def _rows(t, name, K=None, rows=None, dtypes=(torch.bfloat16, torch.float16)):
-    """A 2-D tensor whose rows are 16-byte aligned and contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and
-            (K is None or t.shape[1] == K) and (rows is None or t.shape[0] == rows)):
+def _rows(t, name, K=None, rows=None, dtypes=_HALF):
+    """The row stride of a 2-D tensor whose rows are contiguous and start on
+    16-byte boundaries (of one row, whose stride is arbitrary: K rounded up)."""
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes else ()
+    if len(shape) != 2 or (K is not None and shape[1] != K) or (rows is not None and shape[0] != rows):
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be a {want} [{'rows' if rows is None else rows}, "
                          f"{'K' if K is None else K}] tensor")
-    if t.shape[0] and t.shape[1]:
-        ld = _ld(t)
-        _need((t.stride(1) == 1 or t.shape[1] == 1) and ld >= t.shape[1] and
-              ld * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0,
-              f"{name}'s rows must be contiguous and start on 16-byte boundaries")
-
-
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else _up16(t)
-
-
-def _up16(t):
-    """The smallest aligned stride of a single row, whose own is arbitrary."""
-    e = 16 // t.element_size()
-    return -(-t.shape[1] // e) * e
+    T, K = shape
+    per16 = 16 // t.element_size()
+    ld, step = t.stride()
+    if T <= 1:
+        ld = -(-K // per16) * per16
+    if T and K and (ld < K or ld % per16 or (step != 1 and K != 1) or t.data_ptr() % 16):
+        raise ValueError(f"{name}'s rows must be contiguous and start on 16-byte boundaries")
+    return ld
 
 
 def _span(t):
@@ -117,50 +115,41 @@ def _check_apart(out, name, others, same_ok=False):
         raise ValueError(f"{name} overlaps another tensor of the call")
 
 
-class _Launch:
-    """Device and stream of a call: checks that its tensors share a GPU, makes
-    that device and `stream` current while outputs are allocated and work is
-    queued, and marks tensors of another stream as used on this one."""
+_HERE = contextlib.nullcontext()
 
-    __slots__ = ("stream", "handle", "_dev", "_ctx", "_tensors")
 
-    def __init__(self, tensors, stream):
-        dev = tensors[0].device
-        _need(dev.type == "cuda", f"tensors must be on a GPU, not on {dev}")
+def _on(tensors, stream):
+    """(stream handle, context) of a call: checks that its tensors share a GPU;
+    inside the context that device and `stream` are current, so outputs are
+    allocated there.  Tensors of another stream are marked as used on this one."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors of one call must be on one device: {t.device} and {dev}")
+    _need(dev.type == "cuda", f"tensors must be on a GPU, not on {dev}")
+    if stream is None:
+        # (the public current_stream(dev).cuda_stream is this, behind 2 us of object building)
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        return handle, _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    _need(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
+    if stream != torch.cuda.current_stream(dev):
         for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors of one call must be on one device: {t.device} and {dev}")
-        self._ctx = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-            if torch.cuda.current_device() != dev.index:
-                self._ctx = torch.cuda.device(dev)
-            return
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        _need(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
-        self.handle = stream.cuda_stream
-        self._ctx = torch.cuda.stream(stream)          # makes its device current, too
-        if stream != torch.cuda.current_stream(dev):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)       # makes its device current, too
 
 
-def _fp8_out(rows, K, scales, dev):
-    codes = torch.empty((rows, K), dtype=torch.uint8, device=dev)
+def _fp8_out(rows, K, scales, like):
+    codes = like.new_empty((rows, K), dtype=torch.uint8)
     if scales == "row":
-        return FP8Rows(codes, torch.empty(rows, dtype=torch.float32, device=dev))
-    return FP8Rows(codes, torch.empty((rows, K // 32), dtype=torch.uint8, device=dev))
+        return FP8Rows(codes, like.new_empty((rows,), dtype=torch.float32))
+    return FP8Rows(codes, like.new_empty((rows, K // 32), dtype=torch.uint8))
+
+
+def _check_K(K):
+    _need(8 <= K <= 32768 and K % 8 == 0, f"K must be a multiple of 8 in [8, 32768], not {K}")
 
 
 def _check_scales(scales, K):
@@ -181,16 +170,16 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     total, fp8): y of x's type (want_y, or into `out`); total = s, given with a
     residual (into `total_out`, which like `out` may be x or residual); fp8 the
     8-bit rows when `scales` is "row" or "mx", rounded from the fp32 values."""
-    _rows(x, "x")
+    ldx = _rows(x, "x")
     T, K = x.shape
-    _need(8 <= K <= 32768 and K % 8 == 0, f"K must be a multiple of 8 in [8, 32768], not {K}")
+    _check_K(K)
+    dtype, ldr, lds = x.dtype, 0, 0
     if residual is not None:
-        _rows(residual, "residual", K, T, (x.dtype,))
+        ldr = _rows(residual, "residual", K, T, (dtype,))
     if weight is not None:
-        _need(isinstance(weight, torch.Tensor) and weight.dtype == x.dtype and
-              tuple(weight.shape) == (K,) and weight.is_contiguous() and
-              weight.data_ptr() % 16 == 0,
-              f"weight must be a contiguous 16-byte aligned {x.dtype} [{K}] tensor")
+        _need(isinstance(weight, torch.Tensor) and weight.dtype == dtype and
+              weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0,
+              f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
     if scales is not None:
         _check_scales(scales, K)
     _need(want_y or out is None, "out needs want_y")
@@ -200,28 +189,30 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     eps, weight_offset = float(eps), float(weight_offset)
     _need(0.0 <= eps < 3.4e38 and abs(weight_offset) < 3.4e38,
           "eps must be finite and >= 0, weight_offset finite")
-    given = [x, residual, weight, out, total_out]
+    ldy = K
     if out is not None:
-        _rows(out, "out", K, T, (x.dtype,))
+        ldy = _rows(out, "out", K, T, (dtype,))
         _check_apart(out, "out", (weight, total_out))
         _check_apart(out, "out", (x, residual), True)
-    if total_out is not None:
-        _rows(total_out, "total_out", K, T, (x.dtype,))
-        _check_apart(total_out, "total_out", (weight,))
-        _check_apart(total_out, "total_out", (x, residual), True)
-    with _Launch(given, stream) as on:
-        y = (torch.empty((T, K), dtype=x.dtype, device=x.device) if out is None else out) \
-            if want_y else None
-        total = None
+    if residual is not None:
+        lds = K
+        if total_out is not None:
+            lds = _rows(total_out, "total_out", K, T, (dtype,))
+            _check_apart(total_out, "total_out", (weight,))
+            _check_apart(total_out, "total_out", (x, residual), True)
+    handle, ctx = _on((x, residual, weight, out, total_out), stream)
+    with ctx:
+        y = total = fp8 = codes = sc = None
+        if want_y:
+            y = x.new_empty((T, K)) if out is None else out
         if residual is not None:
-            total = torch.empty((T, K), dtype=x.dtype, device=x.device) \
-                if total_out is None else total_out
-        fp8 = None if scales is None else _fp8_out(T, K, scales, x.device)
-        _lib.rmsnorm(_TYPES[x.dtype], x, _ld(x), residual, 0 if residual is None else _ld(residual),
-                     weight, weight_offset, eps, T, K, total, 0 if total is None else _ld(total),
-                     y, 0 if y is None else _ld(y), _lib.FP8_NONE if fp8 is None else _FP8[scales],
-                     None if fp8 is None else fp8.codes, None if fp8 is None else fp8.scales,
-                     on.handle)
+            total = x.new_empty((T, K)) if total_out is None else total_out
+        kind = _lib.FP8_NONE
+        if scales is not None:
+            kind = _FP8[scales]
+            fp8 = codes, sc = _fp8_out(T, K, scales, x)
+        _lib.rmsnorm(_TYPES[dtype], x, ldx, residual, ldr, weight, weight_offset, eps, T, K,
+                     total, lds, y, ldy, kind, codes, sc, handle)
     return NormOut(y, total, fp8)
 
 
@@ -229,14 +220,15 @@ def quantize_fp8(x: torch.Tensor, scales: str = "mx", *, stream=None) -> FP8Rows
     """bf16 or fp16 rows [rows, K] -> FP8Rows with one fp32 scale per row
     ("row", K a multiple of 8) or one power-of-two scale per 32 elements ("mx",
     a multiple of 32): nvfp4_quantize_rows_fp8.  K is at most 32768."""
-    _rows(x, "x")
+    ldx = _rows(x, "x")
     T, K = x.shape
-    _need(8 <= K <= 32768 and K % 8 == 0, f"K must be a multiple of 8 in [8, 32768], not {K}")
+    _check_K(K)
     _check_scales(scales, K)
-    with _Launch([x], stream) as on:
-        fp8 = _fp8_out(T, K, scales, x.device)
-        _lib.quantize_rows_fp8(_TYPES[x.dtype], x, _ld(x), T, K, _FP8[scales], fp8.codes,
-                               fp8.scales, on.handle)
+    handle, ctx = _on((x,), stream)
+    with ctx:
+        fp8 = _fp8_out(T, K, scales, x)
+        _lib.quantize_rows_fp8(_TYPES[x.dtype], x, ldx, T, K, _FP8[scales], fp8.codes, fp8.scales,
+                               handle)
     return fp8
 
 
@@ -244,35 +236,43 @@ Operand = Union[torch.Tensor, FP8Rows]
 
 
 def _operand(v, name):
-    """(type, values, scales) of a linear operand, checked."""
+    """(type, values, row stride, scales) of a linear operand, checked."""
+    scales = None
     if isinstance(v, torch.Tensor):
-        _rows(v, name)
-        step, kind, scales = 8, _TYPES[v.dtype], None
+        ld = _rows(v, name)
+        step, kind = 8, _TYPES[v.dtype]
+        K = v.shape[1]
     else:
         _need(isinstance(v, tuple) and len(v) == 2,
               f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
         v, scales = v
-        _rows(v, f"{name}.codes", dtypes=(torch.uint8,))
+        ld = _rows(v, name, dtypes=_BYTES)
+        rows, K = v.shape
         _need(isinstance(scales, torch.Tensor) and scales.is_contiguous(),
-              f"{name}.scales must be a contiguous tensor")
+              f"{name}'s scales must be a contiguous tensor")
         if scales.dtype == torch.float32:
-            step, kind, shape = 16, _lib.TYPE_FP8_ROW, (v.shape[0],)
+            step, kind, shape = 16, _lib.TYPE_FP8_ROW, (rows,)
         else:
-            step, kind, shape = 32, _lib.TYPE_FP8_MX, (v.shape[0], v.shape[1] // 32)
-            _need(scales.dtype == torch.uint8, f"{name}.scales must be fp32 or uint8")
-        _need(tuple(scales.shape) == shape, f"{name}.scales must be of shape {shape}")
-    K = v.shape[1]
+            step, kind, shape = 32, _lib.TYPE_FP8_MX, (rows, K // 32)
+            _need(scales.dtype == torch.uint8, f"{name}'s scales must be fp32 or uint8")
+        _need(scales.shape == shape, f"{name}'s scales must be of shape {shape}")
     _need(K >= step and K % step == 0, f"{name} must have a multiple of {step} columns, not {K}")
-    return kind, v, scales
+    return kind, v, ld, scales
 
 
-def _plain(t, name, shape, dtypes=tuple(_TYPES)):
-    """A tensor of `shape` with contiguous rows, without alignment beyond its type's."""
-    _need(isinstance(t, torch.Tensor) and t.dtype in dtypes and tuple(t.shape) == shape and
-          (t.numel() == 0 or ((t.stride(-1) == 1 or t.shape[-1] == 1) and
-                              (t.dim() == 1 or t.shape[0] == 1 or t.stride(0) >= t.shape[1]))),
-          f"{name} must be a {'/'.join(str(d).replace('torch.', '') for d in dtypes)} "
-          f"{list(shape)} tensor with contiguous rows")
+def _plain(t, name, shape, dtypes=_FLOATS):
+    """The row stride of a tensor of `shape` with contiguous rows, aligned to its type."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape:
+        st = t.stride()
+        if len(shape) == 1:
+            if st[0] == 1 or shape[0] <= 1:
+                return 0
+        else:
+            ld = st[0] if shape[0] > 1 else shape[1]
+            if ((st[1] == 1 or shape[1] == 1) and ld >= shape[1]) or 0 in shape:
+                return max(ld, shape[1])
+    raise ValueError(f"{name} must be a {'/'.join(str(d).replace('torch.', '') for d in dtypes)} "
+                     f"{list(shape)} tensor with contiguous rows")
 
 
 def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
@@ -290,55 +290,57 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     type by default, bf16 for FP8Rows), or FP8Rows with "mx" scales for
     out_dtype "mx" (N a multiple of 32).  `out` receives the result and may be
     the residual itself."""
-    kind, av, a_sc = _operand(a, "a")
-    wkind, wv, w_sc = _operand(w, "w")
+    kind, av, lda, a_sc = _operand(a, "a")
+    wkind, wv, ldw, w_sc = _operand(w, "w")
     _need(kind == wkind, "a and w must be of one type, with one kind of scales")
     M, K = av.shape
-    _need(wv.shape[1] == K, f"w must have {K} columns, as a")
-    _need(isinstance(gated, bool), "gated must be True or False")
     rows = wv.shape[0]
+    _need(wv.shape[1] == K, f"w must have {K} columns, as a")
+    _need(gated is False or gated is True, "gated must be True or False")
     _need(not gated or rows % 2 == 0, "a gated w has an even number of rows")
     N = rows // 2 if gated else rows
     try:
         act_id = _ACTS[act]
     except (KeyError, TypeError):
         raise ValueError(f"act must be one of {[k for k in _ACTS]}, not {act!r}") from None
+    bias_type = res_type = ldr = 0
     if bias is not None:
         _plain(bias, "bias", (rows,))
+        bias_type = _TYPES[bias.dtype]
     if residual is not None:
-        _plain(residual, "residual", (M, N))
+        ldr = _plain(residual, "residual", (M, N))
+        res_type = _TYPES[residual.dtype]
     mx = isinstance(out_dtype, str)
+    ldo = N
     if mx:
         _need(out_dtype == "mx", f'out_dtype must be bf16, fp16, fp32 or "mx", not {out_dtype!r}')
         _need(N % 32 == 0, f'an "mx" result needs a multiple of 32 columns, not {N}')
         _need(out is None, 'out is not taken with out_dtype "mx"')
+        out_type = _lib.TYPE_FP8_MX
     else:
         if out_dtype is None:
             out_dtype = out.dtype if isinstance(out, torch.Tensor) else \
                 torch.bfloat16 if a_sc is not None else av.dtype
-        _need(out_dtype in _TYPES, f'out_dtype must be bf16, fp16, fp32 or "mx", not {out_dtype}')
+        out_type = _TYPES.get(out_dtype)
+        _need(out_type is not None, f'out_dtype must be bf16, fp16, fp32 or "mx", not {out_dtype}')
         if out is not None:
-            _plain(out, "out", (M, N), (out_dtype,))
+            ldo = _plain(out, "out", (M, N), (out_dtype,))
             _check_apart(out, "out", (av, wv, a_sc, w_sc, bias))
             _check_apart(out, "out", (residual,), True)
-    with _Launch([av, wv, a_sc, w_sc, bias, residual, out], stream) as on:
-        dev = av.device
+    handle, ctx = _on((av, wv, a_sc, w_sc, bias, residual, out), stream)
+    with ctx:
         out_scales = None
         if mx:
-            res, out_scales = _fp8_out(M, N, "mx", dev)
+            res, out_scales = _fp8_out(M, N, "mx", av)
         else:
-            res = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+            res = av.new_empty((M, N), dtype=out_dtype) if out is None else out
         p = _lib.Linear(
             av.data_ptr(), None if a_sc is None else a_sc.data_ptr(), wv.data_ptr(),
             None if w_sc is None else w_sc.data_ptr(), None if bias is None else bias.data_ptr(),
             None if residual is None else residual.data_ptr(), res.data_ptr(),
-            None if out_scales is None else out_scales.data_ptr(),
-            _ld(av), _ld(wv), 0 if residual is None else max(residual.stride(0), N),
-            max(res.stride(0), N), M, N, K,
-            kind, 0 if bias is None else _TYPES[bias.dtype],
-            0 if residual is None else _TYPES[residual.dtype],
-            _lib.TYPE_FP8_MX if mx else _TYPES[out_dtype], act_id, int(gated))
+            None if out_scales is None else out_scales.data_ptr(), lda, ldw, ldr, ldo, M, N, K,
+            kind, bias_type, res_type, out_type, act_id, gated)
         n = _lib.linear_workspace_size(p)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        _lib.linear(p, ws, n, on.handle)
+        ws = av.new_empty((n,), dtype=torch.uint8) if n else None
+        _lib.linear(p, ws, n, handle)
     return FP8Rows(res, out_scales) if mx else res

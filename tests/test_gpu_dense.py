@@ -222,7 +222,7 @@ def operand(shape, seed, kind, scale):
 def scaled(M, kind, out):
     """Whether linear runs the scaled 8-bit instruction (more than a few rows, an
     output that fp32's accuracy would be lost on)."""
-    return kind in ("row", "mx") and M > 64 and out != F32
+    return kind in ("row", "mx") and M > 64 and out in (None, BF16, F16)
 
 
 def linear_case(M, N, K, kind, act=None, gated=False, bias=None, residual=None, out=None, seed=0):
