@@ -331,9 +331,8 @@ __device__ __forceinline__ f32x4 mma(const Prepared<kKind, kByte>& w, const Prep
   return acc;
 }
 
-// 16 scales of a row, of the four steps from block `at` on, as four words, one per
-// block of a step (byte t: step t).  Past the end of the row the data are zeros:
-// any scale does.
+// 16 scales of a row, of the four steps from block `at` on (past the end of the
+// row the data are zeros: any scale does) ...
 __device__ __forceinline__ u32x4 load_scales(const uint8_t* row, int at, int nblk) {
   u32x4 d;
   if (at + 16 <= nblk) {
@@ -342,12 +341,17 @@ __device__ __forceinline__ u32x4 load_scales(const uint8_t* row, int at, int nbl
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       uint32_t w = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) w |= (at + 4 * t + b < nblk ? (uint32_t)row[at + 4 * t + b] : 127u) << (8 * b);
+#pragma unroll 1                                                  // (once per tile: few registers matter more)
+      for (int b = 0; b < 4; ++b) w = (w >> 8) | ((at + 4 * t + b < nblk ? (uint32_t)row[at + 4 * t + b] : 127u) << 24);
       d[t] = w;
     }
   }
-  // 4 x 4 bytes transposed
+  return d;
+}
+
+// ... and as four words, one per block of a step (byte t: step t): 4 x 4 bytes
+// transposed.
+__device__ __forceinline__ u32x4 scale_words(const u32x4& d) {
   const uint32_t lo01 = __builtin_amdgcn_perm(d.y, d.x, 0x05010400u), hi01 = __builtin_amdgcn_perm(d.y, d.x, 0x07030602u);
   const uint32_t lo23 = __builtin_amdgcn_perm(d.w, d.z, 0x05010400u), hi23 = __builtin_amdgcn_perm(d.w, d.z, 0x07030602u);
   return u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100u), __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
@@ -386,7 +390,7 @@ __device__ __forceinline__ void step_barrier() {
 // the sums through LDS, 32 rows of each wavefront at a time, so that every thread
 // finishes 8 consecutive outputs of a row and whole rows are stored.
 template <int kKind, int kBM, int kBN, int kWM, int kWN, bool kGated>
-__global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinParams p) {
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const LinParams p) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kTM = kBM / kWM, kTN = kBN / kWN;
   constexpr int kFM = kTM / 16, kFN = kTN / 16;
@@ -394,7 +398,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
   constexpr int kStage = (kBM + kBN) * kStep;
   constexpr int kLoads = (kBM + kBN) / 8 / kWaves;             // 1 KiB copies per wavefront and step
   static_assert((kBM + kBN) / 8 % kWaves == 0 && kBM / 8 % kLoads == 0, "whole copies; a wavefront copies one operand");
-  static_assert(!kGated || kOutN % (8 * kLoads) == 0 || 8 * kLoads % kOutN == 0, "a copy holds gate or up rows");
+  static_assert(!kGated || kOutN % (8 * kLoads) == 0 || 8 * kLoads == kBN, "copies by gate and up rows");
   constexpr bool kScaled = is_block8(kKind);
   static_assert(kBM + kBN == 64 * kWaves || !kScaled, "a thread loads the scales of one row");
   __shared__ __align__(1024) char smem[2 * kStage];
@@ -422,42 +426,43 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
   const int64_t m0 = (int64_t)tm * kBM;
   const int32_t n0 = tn * kOutN;
 
-  // source of each copy: lane -> (row of the tile, chunk), as an offset from the
-  // tile's first row; rows past the edge repeat the last row, their results are
-  // not stored
-  uint32_t off[kLoads];
-  uint64_t src[kLoads];                                        // uniform: the operand's tile (and half) at this step
+  // source of each copy: lane -> (row of the operand's tile, chunk).  Rows past the
+  // edge repeat the last row, their results are not stored.  The offset from the
+  // tile's first row is formed at each copy (three instructions): kept for all
+  // copies, it would cost the registers that the fragments need.
+  constexpr int kHalves = kGated && 8 * kLoads > kOutN ? 2 : 1;  // a wavefront's copies hold gate and up rows
+  uint64_t base[kHalves];                                      // uniform: the operand's tile at this step
   const int chunk = (lane & 7) ^ (lane >> 3);                  // (row & 7) == lane >> 3
-  const bool is_a = wave * kLoads * 8 < kBM;
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int r = (wave * kLoads + i) * 8 + (lane >> 3);
-    if (is_a) {
-      const int32_t last = (int32_t)min((int64_t)kBM, p.M - m0) - 1;
-      src[i] = reinterpret_cast<uint64_t>(p.a + m0 * p.lda);
-      off[i] = (uint32_t)(r < last ? r : last) * (uint32_t)p.lda + chunk * 16;
-    } else {
-      const int c = (r - kBM) % kOutN, last = min(kOutN, p.N - n0) - 1;
-      const bool up = (wave * kLoads + i) * 8 - kBM >= kOutN;      // the same for the copy's 8 rows
-      src[i] = reinterpret_cast<uint64_t>(p.w + ((int64_t)n0 + (up ? p.N : 0)) * p.ldw);
-      off[i] = (uint32_t)(c < last ? c : last) * (uint32_t)p.ldw + chunk * 16;
-    }
+  const int first = wave * kLoads * 8;                         // the wavefront's first row of the tile
+  const bool is_a = first < kBM;
+  int row0 = (is_a ? first : (first - kBM) % kOutN) + (lane >> 3);
+  const int last_row = is_a ? (int)min((int64_t)kBM, p.M - m0) - 1 : min(kOutN, p.N - n0) - 1;
+  const uint32_t ld = (uint32_t)(is_a ? p.lda : p.ldw);
+  {
+    const int64_t up = kGated && !is_a ? (first - kBM) / kOutN * (int64_t)p.N : 0;
+    base[0] = reinterpret_cast<uint64_t>(is_a ? p.a + m0 * p.lda : p.w + (n0 + up) * p.ldw);
+    if (kHalves == 2) base[kHalves - 1] = is_a ? base[0] : reinterpret_cast<uint64_t>(p.w + ((int64_t)n0 + p.N) * p.ldw);
   }
   const int steps = (p.kbytes + kStep - 1) / kStep;
   const int tail = p.kbytes - (steps - 1) * kStep;             // bytes of the last step
   auto fetch = [&](int ks) {
     char* dst = smem + (ks & 1) * kStage + wave * kLoads * 1024;
     if (chunk * 16 < (ks == steps - 1 ? tail : kStep)) {
+      asm volatile("" : "+v"(row0));                           // (formed here, not carried along)
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) load_lds16(reinterpret_cast<const char*>(src[i]) + off[i], dst + i * 1024);
+      for (int i = 0; i < kLoads; ++i) {
+        const int add = kHalves == 2 && !is_a ? 8 * i % kOutN : 8 * i;
+        const uint32_t off = (uint32_t)min(row0 + add, last_row) * ld + chunk * 16;
+        load_lds16(reinterpret_cast<const char*>(base[kHalves == 2 ? 8 * i / kOutN : 0]) + off, dst + i * 1024);
+      }
     } else {                                                   // past the end of the rows
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(dst + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      src[i] += kStep;
-      asm volatile("" : "+s"(src[i]));                         // kept in scalar registers, apart from the lanes' offsets
+    for (int i = 0; i < kHalves; ++i) {
+      base[i] += kStep;
+      asm volatile("" : "+s"(base[i]));
     }
   };
 
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
   // scales), for the byte of the scales and the slots of fa when a step has only
   // two groups.
   static_assert(kFM == 2 || kFM % 4 == 0, "fragment slots");
-  constexpr int kUnroll = kScaled ? 4 : 2;
+  constexpr int kAhead = kFM == 8 && kKind >= kRow8 ? 1 : 2;   // 8-bit fragments: one group, for want of registers
   constexpr int kWords = kKind == kBlock8Wide ? 2 : 1;         // scale words of a lane and row
   Frag fa[4], fw[kFN];
   uint32_t va[kFM][2], vw[kFN][2];
@@ -526,7 +531,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
     for (int j = 0; j < kFN; ++j) pw[j].set(fw[j], vw[j]);
 #pragma unroll
     for (int i = 0; i < kFM - 2; ++i) {
-      fa[(kBase + i + 2) & 3] = read_frag(ta, (i + 2) * 16 + i16, g);
+      if (kAhead == 1) fa[(kBase + i + 1) & 3] = read_frag(ta, (i + 1) * 16 + i16, g);
+      if (kAhead == 2 || i == kFM - 3) fa[(kBase + i + 2) & 3] = read_frag(ta, (i + 2) * 16 + i16, g);
       __builtin_amdgcn_sched_barrier(0);
       Op pa;
       pa.set(fa[(kBase + i) & 3], va[i]);
@@ -538,7 +544,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
       // the next four steps' scales: loaded a step before they go to LDS, which
       // is a step before they are read
       if constexpr (T == 1) scale_next = load_scales(scale_row, 4 * (ks + 3), nblk);
-      if constexpr (T == 2) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_next;
+      if constexpr (T == 2) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_words(scale_next);
     }
     step_barrier();                                            // this buffer is read, the other one filled
     if (ks + 2 < steps) fetch(ks + 2);
@@ -547,7 +553,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
     pa[1].set(fa[(kBase + kFM - 1) & 3], va[kFM - 1]);
     // (after the last step these read an older one, unused)
     fa[kNext] = read_frag(na, i16, g);
-    fa[kNext + 1] = read_frag(na, 16 + i16, g);
+    if (kAhead == 2) fa[kNext + 1] = read_frag(na, 16 + i16, g);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
@@ -559,18 +565,22 @@ __global__ __launch_bounds__(64 * kWM * kWN) void linear_tile_kernel(const LinPa
   };
   fetch(0);
   if (steps > 1) fetch(1);
-  if constexpr (kScaled) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = load_scales(scale_row, 0, nblk);
+  if constexpr (kScaled) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = scale_words(load_scales(scale_row, 0, nblk));
   step_barrier();
 #pragma unroll
   for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + (kBM + wn * kTN) * kStep, j * 16 + i16, g);
   fa[0] = read_frag(smem + wm * kTM * kStep, i16, g);
-  fa[1] = read_frag(smem + wm * kTM * kStep, 16 + i16, g);
-  for (int ks = 0; ks < steps; ks += kUnroll) {
+  if (kAhead == 2) fa[1] = read_frag(smem + wm * kTM * kStep, 16 + i16, g);
+  for (int ks = 0;;) {
     step(std::integral_constant<int, 0>{}, ks);
-    if (ks + 1 < steps) step(std::integral_constant<int, 1>{}, ks + 1);
-    if constexpr (kUnroll == 4) {
-      if (ks + 2 < steps) step(std::integral_constant<int, 2>{}, ks + 2);
-      if (ks + 3 < steps) step(std::integral_constant<int, 3>{}, ks + 3);
+    if (++ks == steps) break;
+    step(std::integral_constant<int, 1>{}, ks);
+    if (++ks == steps) break;
+    if constexpr (kScaled) {
+      step(std::integral_constant<int, 2>{}, ks);
+      if (++ks == steps) break;
+      step(std::integral_constant<int, 3>{}, ks);
+      if (++ks == steps) break;
     }
   }
 
