@@ -628,9 +628,9 @@ typedef enum {
  *                  to out_scales uint8 [M, N/32]).
  * bias_type, residual_type: BF16, FP16 or FP32, each independent of the others.
  * out may be residual itself (same pointer, type and stride); it must not
- * overlap any input in another way.  M == 0 or N == 0 is a no-op.  K, N <= 2^24
- * and ceil(M / 256) * ceil(N' / 256) <= 2^22 with N' the rows of w, else
- * NVFP4_ERR_UNSUPPORTED.
+ * overlap any input in another way.  M == 0 or N == 0 is a no-op.  K <= 2^22,
+ * N <= 2^24, row strides of a and w <= 2^23 bytes and ceil(M / 256) *
+ * ceil(N' / 256) <= 2^22 with N' the rows of w, else NVFP4_ERR_UNSUPPORTED.
  */
 typedef struct {
   const void* a;

@@ -30,17 +30,28 @@ bool is_float_type(int32_t t) { return t == NVFP4_TYPE_BF16 || t == NVFP4_TYPE_F
 size_t float_size(int32_t t) { return t == NVFP4_TYPE_FP32 ? 4 : 2; }
 bool is_fp8(int32_t t) { return t == NVFP4_TYPE_FP8_ROW || t == NVFP4_TYPE_FP8_MX; }
 
-// The sizes alone; what nvfp4_linear_workspace_size needs.
-nvfp4_status_t check_linear_sizes(const nvfp4_linear_t* p) {
+int32_t elem_type(int32_t t) {
+  return t == NVFP4_TYPE_BF16 ? 0 : t == NVFP4_TYPE_FP16 ? 1 : t == NVFP4_TYPE_FP32 ? 2 : 3;
+}
+
+// Sizes and types alone (no pointer of *p is looked at), as nvfp4_linear_workspace_size
+// and nvfp4_linear both need them.
+nvfp4_status_t check_linear_sizes(const nvfp4_linear_t* p, LinearArgs* a) {
   if (!p || p->M < 0 || p->N < 0 || p->K < 1) return NVFP4_ERR_INVALID_ARG;
   if (p->type != NVFP4_TYPE_BF16 && p->type != NVFP4_TYPE_FP16 && !is_fp8(p->type)) return NVFP4_ERR_INVALID_ARG;
   if (p->K % (p->type == NVFP4_TYPE_FP8_MX ? 32 : is_fp8(p->type) ? 16 : 8)) return NVFP4_ERR_INVALID_ARG;
   if (p->act < NVFP4_ACT_NONE || p->act > NVFP4_ACT_RELU || (p->gated != 0 && p->gated != 1))
     return NVFP4_ERR_INVALID_ARG;
-  // 32-bit sizes inside the kernels: bytes of a row, rows of w, tiles of a launch
-  if (p->K > (1 << 24) || p->N > (1 << 24)) return NVFP4_ERR_UNSUPPORTED;
+  if (!is_float_type(p->out_type) && p->out_type != NVFP4_TYPE_FP8_MX) return NVFP4_ERR_INVALID_ARG;
+  if (p->out_type == NVFP4_TYPE_FP8_MX && p->N % 32) return NVFP4_ERR_INVALID_ARG;
+  // 32-bit sizes inside the kernels: a tile's offsets, rows of w, tiles of a launch
+  if (p->K > (1 << 22) || p->N > (1 << 24)) return NVFP4_ERR_UNSUPPORTED;
   const int64_t tiles = (((int64_t)p->M + 255) / 256) * (((int64_t)p->N * (p->gated + 1) + 255) / 256);
   if (tiles > (1 << 22)) return NVFP4_ERR_UNSUPPORTED;
+  a->M = p->M; a->N = p->N; a->K = p->K;
+  a->kind = p->type == NVFP4_TYPE_BF16 ? 0 : p->type == NVFP4_TYPE_FP16 ? 1 : p->type == NVFP4_TYPE_FP8_ROW ? 2 : 3;
+  a->act = p->act; a->gated = p->gated;
+  a->out_type = elem_type(p->out_type);
   return NVFP4_OK;
 }
 
@@ -100,25 +111,26 @@ NVFP4_API nvfp4_status_t nvfp4_quantize_rows_fp8(int32_t type, const void* x, in
 
 NVFP4_API nvfp4_status_t nvfp4_linear_workspace_size(const nvfp4_linear_t* p, size_t* bytes) {
   if (!bytes) return NVFP4_ERR_INVALID_ARG;
-  const nvfp4_status_t st = check_linear_sizes(p);
+  LinearArgs a = {};
+  const nvfp4_status_t st = check_linear_sizes(p, &a);
   if (st != NVFP4_OK) return st;
-  *bytes = linear_workspace_bytes(p->M, p->N, p->K, p->type == NVFP4_TYPE_BF16 ? 0 : p->type == NVFP4_TYPE_FP16 ? 1 : p->type == NVFP4_TYPE_FP8_ROW ? 2 : 3, p->gated);
+  *bytes = linear_workspace_bytes(a);
   return NVFP4_OK;
 }
 
 NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, size_t workspace_bytes,
                                       nvfp4_stream_t stream) {
-  nvfp4_status_t st = check_linear_sizes(p);
+  LinearArgs a = {};
+  const nvfp4_status_t st = check_linear_sizes(p, &a);
   if (st != NVFP4_OK) return st;
-  if (!is_float_type(p->out_type) && p->out_type != NVFP4_TYPE_FP8_MX) return NVFP4_ERR_INVALID_ARG;
   if (p->bias && !is_float_type(p->bias_type)) return NVFP4_ERR_INVALID_ARG;
   if (p->residual && !is_float_type(p->residual_type)) return NVFP4_ERR_INVALID_ARG;
-  if (p->out_type == NVFP4_TYPE_FP8_MX && p->N % 32) return NVFP4_ERR_INVALID_ARG;
   if (p->M == 0 || p->N == 0) return NVFP4_OK;
   const bool f8 = is_fp8(p->type);
   const int64_t esz = f8 ? 1 : 2;
   if (!p->a || !p->w || !p->out || !aligned(p->a, 16) || !aligned(p->w, 16)) return NVFP4_ERR_INVALID_ARG;
   if (p->lda < p->K || p->ldw < p->K || p->lda * esz % 16 || p->ldw * esz % 16) return NVFP4_ERR_INVALID_ARG;
+  if (p->lda * esz > (1 << 23) || p->ldw * esz > (1 << 23)) return NVFP4_ERR_UNSUPPORTED;
   if (f8 && (!p->a_scales || !p->w_scales)) return NVFP4_ERR_INVALID_ARG;
   if (p->type == NVFP4_TYPE_FP8_ROW && (!aligned(p->a_scales, 4) || !aligned(p->w_scales, 4)))
     return NVFP4_ERR_INVALID_ARG;
@@ -131,16 +143,11 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, 
   } else if (!aligned(p->out, float_size(p->out_type))) {
     return NVFP4_ERR_INVALID_ARG;
   }
-  LinearArgs a = {};
   a.a = p->a; a.a_scales = p->a_scales; a.w = p->w; a.w_scales = p->w_scales;
   a.bias = p->bias; a.residual = p->residual; a.out = p->out; a.out_scales = p->out_scales;
   a.lda = p->lda; a.ldw = p->ldw; a.ldr = p->ldr; a.ldo = p->ldo;
-  a.M = p->M; a.N = p->N; a.K = p->K;
-  a.kind = p->type == NVFP4_TYPE_BF16 ? 0 : p->type == NVFP4_TYPE_FP16 ? 1 : p->type == NVFP4_TYPE_FP8_ROW ? 2 : 3;
-  a.act = p->act; a.gated = p->gated;
-  auto elem = [](int32_t t) { return t == NVFP4_TYPE_BF16 ? 0 : t == NVFP4_TYPE_FP16 ? 1 : t == NVFP4_TYPE_FP32 ? 2 : 3; };
-  a.bias_type = elem(p->bias_type); a.residual_type = elem(p->residual_type); a.out_type = elem(p->out_type);
-  const size_t need = linear_workspace_bytes(a.M, a.N, a.K, a.kind, a.gated);
+  a.bias_type = elem_type(p->bias_type); a.residual_type = elem_type(p->residual_type);
+  const size_t need = linear_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return NVFP4_ERR_WORKSPACE;
   return device_status(launch_linear(a, workspace, static_cast<hipStream_t>(stream)));
 }

@@ -142,6 +142,6 @@ struct LinearArgs {
   int32_t kind, act, gated, bias_type, residual_type, out_type;
 };
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream);
-size_t linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t kind, int32_t gated);
+size_t linear_workspace_bytes(const LinearArgs& a);   // reads sizes, kind, out_type and gated
 
 }  // namespace nvfp4

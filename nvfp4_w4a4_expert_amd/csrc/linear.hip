@@ -20,6 +20,7 @@
 // fp32's own error.  fp32 outputs of 8-bit operands therefore run on the bf16
 // instruction: an E4M3 value times a power of two is a bf16 number, the products
 // are exact and the sums are fp32 sums (the "wide" kinds, at half the rate).
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -56,6 +57,10 @@ struct LinParams {
   int32_t M, N, kbytes;
   int32_t act, bias_type, residual_type, out_type;
   int32_t tiles_m, tiles_n;
+  // tiles whole .. tiles_m * tiles_n - 1 are computed in `parts` parts of part_steps
+  // K steps, whose sums go to partial[tile - whole][part][rows][columns]
+  int32_t whole, parts, part_steps;
+  float* partial;
 };
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int32_t type) {
@@ -185,14 +190,62 @@ struct Columns {
   }
 };
 
+// kLen residual elements of row m, held as they were loaded, so that the loads of
+// several rows are in flight together.
 template <int kLen>
-__device__ __forceinline__ void add_residual(const LinParams& p, int64_t m, int32_t n, float* v) {
-  if (!p.residual) return;
-  float r[kLen];
-  load_run<kLen>(p.residual, m * p.ldr + n, p.residual_type, p.N - n, r);
+struct Residual {
+  uint32_t d[kLen];                                              // 16-bit types: the first half
+
+  __device__ __forceinline__ void load(const LinParams& p, int64_t m, int32_t n) {
+    if (!p.residual || n >= p.N) return;
+    const int64_t at = m * p.ldr + n;
+    const int have = p.N - n;
+    const bool wide = p.residual_type == kOutF32;
+    const char* src = static_cast<const char*>(p.residual) + at * (wide ? 4 : 2);
+    if (have >= kLen && (reinterpret_cast<uintptr_t>(src) & (kLen >= 8 ? 15 : 7)) == 0) {
+      if constexpr (kLen >= 8) {
 #pragma unroll
-  for (int i = 0; i < kLen; ++i) v[i] += r[i];
-}
+        for (int i = 0; i < kLen / 2; i += 4) *reinterpret_cast<u32x4*>(d + i) = *reinterpret_cast<const u32x4*>(src + 4 * i);
+        if (wide) {
+#pragma unroll
+          for (int i = kLen / 2; i < kLen; i += 4) *reinterpret_cast<u32x4*>(d + i) = *reinterpret_cast<const u32x4*>(src + 4 * i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLen / 2; i += 2) *reinterpret_cast<uint2*>(d + i) = *reinterpret_cast<const uint2*>(src + 4 * i);
+        if (wide) {
+#pragma unroll
+          for (int i = kLen / 2; i < kLen; i += 2) *reinterpret_cast<uint2*>(d + i) = *reinterpret_cast<const uint2*>(src + 4 * i);
+        }
+      }
+    } else if (wide) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i)
+        if (i < have) d[i] = reinterpret_cast<const uint32_t*>(src)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLen / 2; ++i) {
+        const uint32_t lo = 2 * i < have ? reinterpret_cast<const uint16_t*>(src)[2 * i] : 0;
+        const uint32_t hi = 2 * i + 1 < have ? reinterpret_cast<const uint16_t*>(src)[2 * i + 1] : 0;
+        d[i] = lo | (hi << 16);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void add(const LinParams& p, float* v) const {
+    if (!p.residual) return;
+    if (p.residual_type == kOutF32) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) v[i] += __uint_as_float(d[i]);
+    } else if (p.residual_type == kOutF16) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) v[i] += (float)__builtin_bit_cast(_Float16, (uint16_t)(d[i / 2] >> (16 * (i & 1))));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) v[i] += (i & 1) ? bf16_hi(d[i / 2]) : bf16_lo(d[i / 2]);
+    }
+  }
+};
 
 // kLen consecutive outputs of row m from column n on, each rounded once; wide
 // stores where the row's alignment and the tensor's edge allow them.
@@ -307,28 +360,25 @@ struct Prepared<kRow8Wide, kByte> : PreparedWide<kByte> {};
 template <int kByte>
 struct Prepared<kBlock8Wide, kByte> : PreparedWide<kByte> {};
 
-// acc += w . a over a K step; w is the row operand, so a lane's four results are
-// four consecutive output columns (instruction rows 4g .. 4g + 3) of one row of a.
+// acc += w . a over the s-th of a K step's kSubs parts; w is the row operand, so a
+// lane's four results are four consecutive output columns (instruction rows 4g ..
+// 4g + 3) of one row of a.
+template <int kKind>
+constexpr int kSubs = is_wide(kKind) ? 4 : kKind == kRow8 || kKind == kBlock8 ? 1 : 2;
+
 template <int kKind, int kByte>
-__device__ __forceinline__ f32x4 mma(const Prepared<kKind, kByte>& w, const Prepared<kKind, kByte>& a, f32x4 acc) {
-  if constexpr (is_wide(kKind)) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[t], a.v[t], acc, 0, 0, 0);
-  } else if constexpr (kKind == kBf16) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.f.c[t]),
-                                                    __builtin_bit_cast(bf16x8_t, a.f.c[t]), acc, 0, 0, 0);
-  } else if constexpr (kKind == kF16) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w.f.c[t]),
-                                                   __builtin_bit_cast(half8_t, a.f.c[t]), acc, 0, 0, 0);
-  } else {
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8_t, w.f), __builtin_bit_cast(i32x8_t, a.f),
-                                                           acc, 0, 0, kByte, (int)w.scale, kByte, (int)a.scale);
-  }
-  return acc;
+__device__ __forceinline__ f32x4 mma(const Prepared<kKind, kByte>& w, const Prepared<kKind, kByte>& a, int s, f32x4 acc) {
+  if constexpr (is_wide(kKind))
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[s], a.v[s], acc, 0, 0, 0);
+  else if constexpr (kKind == kBf16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w.f.c[s]),
+                                                   __builtin_bit_cast(bf16x8_t, a.f.c[s]), acc, 0, 0, 0);
+  else if constexpr (kKind == kF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w.f.c[s]),
+                                                  __builtin_bit_cast(half8_t, a.f.c[s]), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8_t, w.f), __builtin_bit_cast(i32x8_t, a.f),
+                                                            acc, 0, 0, kByte, (int)w.scale, kByte, (int)a.scale);
 }
 
 // 16 scales of a row, of the four steps from block `at` on (past the end of the
@@ -369,27 +419,55 @@ __device__ __forceinline__ Frag read_frag(const char* tile, int row, int g) {
   return f;
 }
 
-__device__ __forceinline__ void load_lds16(const char* src, char* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// Copies 16 bytes per lane from base + off to consecutive places in LDS from `lds`
+// on.  Written out because the compiler, where it knows of such a copy, waits for
+// all of them before the next LDS read, and the copies of later steps must stay on
+// their way.  No register receives the data; step_barrier() waits for it.
+__device__ __forceinline__ void copy_lds16(uint64_t base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)p);
 }
 
 // Barrier at the turn of a step: this wavefront's copies into LDS have arrived
 // and its LDS reads are done before any wavefront passes.  The wait is written
 // out because the copies are counted with memory loads, whose completion a
 // workgroup barrier by itself does not ask for.
+// kLeft: copies of later steps that may still be on their way.
+template <int kLeft>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  static_assert(kLeft < 64, "the counter's width");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLeft) : "memory");
   lds_barrier();
+}
+
+// The g-th of `total` workgroups in an order that gives each of the 8 XCDs (which
+// receive workgroups in turn) a contiguous range.
+__device__ __forceinline__ int32_t xcd_order(int32_t g, int32_t total) {
+  const int32_t per = total / 8, rest = total % 8, xcd = g % 8;
+  return xcd * per + (xcd < rest ? xcd : rest) + g / 8;
+}
+
+// Tile number -> (tile row, tile column): bands of 8 tile rows, each walked down
+// its columns, so that neighbours share rows of a and of w in their L2.
+__device__ __forceinline__ void tile_at(const LinParams& p, int32_t t, int32_t& tm, int32_t& tn) {
+  constexpr int32_t kBand = 8;
+  const int32_t band = t / (kBand * p.tiles_n);
+  const int32_t rows = min(kBand, p.tiles_m - band * kBand);
+  const int32_t in = t - band * kBand * p.tiles_n;
+  tm = band * kBand + in % rows;
+  tn = in / rows;
 }
 
 // ---- tiled kernel -------------------------------------------------------------
 // A workgroup of kWM x kWN wavefronts owns kBM rows of a and kBN rows of w
 // (gated: kBN / 2 output columns, their gate rows, then their up rows).  Each K
-// step's rows are copied straight into LDS (two buffers).  The epilogue passes
+// step's rows are copied straight into LDS (kStages buffers).  The epilogue passes
 // the sums through LDS, 32 rows of each wavefront at a time, so that every thread
 // finishes 8 consecutive outputs of a row and whole rows are stored.
-template <int kKind, int kBM, int kBN, int kWM, int kWN, bool kGated>
+template <int kKind, int kBM, int kBN, int kWM, int kWN, int kStages, bool kGated>
 __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const LinParams p) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kTM = kBM / kWM, kTN = kBN / kWN;
@@ -398,31 +476,33 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   constexpr int kStage = (kBM + kBN) * kStep;
   constexpr int kLoads = (kBM + kBN) / 8 / kWaves;             // 1 KiB copies per wavefront and step
   static_assert((kBM + kBN) / 8 % kWaves == 0 && kBM / 8 % kLoads == 0, "whole copies; a wavefront copies one operand");
-  static_assert(!kGated || kOutN % (8 * kLoads) == 0 || 8 * kLoads == kBN, "copies by gate and up rows");
+  static_assert(!kGated || kOutN % (8 * kLoads) == 0, "a wavefront copies gate or up rows");
   constexpr bool kScaled = is_block8(kKind);
-  static_assert(kBM + kBN == 64 * kWaves || !kScaled, "a thread loads the scales of one row");
-  __shared__ __align__(1024) char smem[2 * kStage];
+  static_assert(kBM + kBN <= 64 * kWaves || !kScaled, "a thread loads the scales of one row");
+  static_assert((kStages & (kStages - 1)) == 0, "buffer of a step by masking");
+  __shared__ __align__(1024) char smem[kStages * kStage];
   __shared__ __align__(16) uint32_t s_scale[kScaled ? 2 : 1][kScaled ? kBM + kBN : 1][4];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int wm = wave / kWN, wn = wave % kWN;
 
-  // tiles: each of the 8 XCDs gets a contiguous range of them (workgroups are
-  // dealt to the XCDs in turn), walked in groups of 8 tile rows
-  int32_t tm, tn;
-  {
-    const int32_t total = p.tiles_m * p.tiles_n;
-    const int32_t per = total / 8, rest = total % 8;
-    const int32_t xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-    const int32_t t = xcd * per + (xcd < rest ? xcd : rest) + at;
-    constexpr int32_t kGroup = 8;
-    const int32_t band = t / (kGroup * p.tiles_n);
-    const int32_t rows = min(kGroup, p.tiles_m - band * kGroup);
-    const int32_t in = t - band * kGroup * p.tiles_n;
-    tm = band * kGroup + in % rows;
-    tn = in / rows;
+  // this workgroup's tile and K steps: all of them, or a part's
+  const int32_t total = p.tiles_m * p.tiles_n;
+  const bool whole = (int32_t)blockIdx.x < p.whole;
+  int32_t tile_no, part = 0, tm, tn;
+  if (whole) {
+    tile_no = xcd_order(blockIdx.x, p.whole);
+  } else {
+    const int32_t left = total - p.whole;
+    const int32_t q = xcd_order(blockIdx.x - p.whole, left * p.parts);
+    part = q / left;
+    tile_no = p.whole + q % left;
   }
+  tile_at(p, tile_no, tm, tn);
+  const int step0 = part * p.part_steps;
+  const int all_steps = (p.kbytes + kStep - 1) / kStep;
+  const int steps = whole ? all_steps : min(p.part_steps, all_steps - step0);
   const int64_t m0 = (int64_t)tm * kBM;
   const int32_t n0 = tn * kOutN;
 
@@ -430,40 +510,31 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   // edge repeat the last row, their results are not stored.  The offset from the
   // tile's first row is formed at each copy (three instructions): kept for all
   // copies, it would cost the registers that the fragments need.
-  constexpr int kHalves = kGated && 8 * kLoads > kOutN ? 2 : 1;  // a wavefront's copies hold gate and up rows
-  uint64_t base[kHalves];                                      // uniform: the operand's tile at this step
   const int chunk = (lane & 7) ^ (lane >> 3);                  // (row & 7) == lane >> 3
   const int first = wave * kLoads * 8;                         // the wavefront's first row of the tile
   const bool is_a = first < kBM;
   int row0 = (is_a ? first : (first - kBM) % kOutN) + (lane >> 3);
   const int last_row = is_a ? (int)min((int64_t)kBM, p.M - m0) - 1 : min(kOutN, p.N - n0) - 1;
   const uint32_t ld = (uint32_t)(is_a ? p.lda : p.ldw);
-  {
-    const int64_t up = kGated && !is_a ? (first - kBM) / kOutN * (int64_t)p.N : 0;
-    base[0] = reinterpret_cast<uint64_t>(is_a ? p.a + m0 * p.lda : p.w + (n0 + up) * p.ldw);
-    if (kHalves == 2) base[kHalves - 1] = is_a ? base[0] : reinterpret_cast<uint64_t>(p.w + ((int64_t)n0 + p.N) * p.ldw);
-  }
-  const int steps = (p.kbytes + kStep - 1) / kStep;
-  const int tail = p.kbytes - (steps - 1) * kStep;             // bytes of the last step
+  const int64_t up = kGated && !is_a ? (first - kBM) / kOutN * (int64_t)p.N : 0;
+  uint64_t base = reinterpret_cast<uint64_t>((is_a ? p.a + m0 * p.lda : p.w + (n0 + up) * p.ldw) + (int64_t)step0 * kStep);
+  // bytes of the last step
+  const int tail = min(p.kbytes - (step0 + steps - 1) * kStep, kStep);
   auto fetch = [&](int ks) {
-    char* dst = smem + (ks & 1) * kStage + wave * kLoads * 1024;
+    char* dst = smem + (ks & (kStages - 1)) * kStage + wave * kLoads * 1024;
     if (chunk * 16 < (ks == steps - 1 ? tail : kStep)) {
+      const uint32_t to = lds_address(dst);
       asm volatile("" : "+v"(row0));                           // (formed here, not carried along)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int add = kHalves == 2 && !is_a ? 8 * i % kOutN : 8 * i;
-        const uint32_t off = (uint32_t)min(row0 + add, last_row) * ld + chunk * 16;
-        load_lds16(reinterpret_cast<const char*>(base[kHalves == 2 ? 8 * i / kOutN : 0]) + off, dst + i * 1024);
+        const uint32_t off = (uint32_t)min(row0 + 8 * i, last_row) * ld + chunk * 16;
+        copy_lds16(base, off, to + i * 1024);
       }
     } else {                                                   // past the end of the rows
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(dst + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
     }
-#pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      base[i] += kStep;
-      asm volatile("" : "+s"(base[i]));
-    }
+    base += kStep;
   };
 
   f32x4 acc[kFN][kFM];
@@ -478,7 +549,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   const uint8_t* scale_row = nullptr;
   u32x4 scale_next;
   if constexpr (kScaled) {
-    const int r = threadIdx.x;
+    const int r = min((int)threadIdx.x, kBM + kBN - 1);
     if (r < kBM) {
       scale_row = static_cast<const uint8_t*>(p.a_scales) + min(m0 + r, (int64_t)p.M - 1) * nblk;
     } else {
@@ -489,13 +560,12 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   }
 
   // Main loop.  A step runs its groups of instructions (one 16-row fragment of a
-  // with all of w) in order, the fragments of a being read two groups ahead; the
-  // last two groups run fragment of w by fragment of w.  The barrier falls before
-  // them: behind it the buffer that the step has read is refilled for the step
-  // after next, and each fragment of w is replaced by the next step's as soon as
+  // with all of w) in order, the fragments of a being read kAhead groups ahead; the
+  // last kAhead groups run fragment of w by fragment of w.  The barrier falls before
+  // them: behind it the buffer that the step has read is refilled for a later
+  // step, and each fragment of w is replaced by the next step's as soon as
   // its last instruction is issued, so the matrix unit does not wait for LDS at
-  // the turn of a step.  The scheduling barriers keep the compiler from moving
-  // the reads back to their uses.  T: the step's number modulo 4 (2 without block
+  // the turn of a step.  T: the step's number modulo 4 (2 without block
   // scales), for the byte of the scales and the slots of fa when a step has only
   // two groups.
   static_assert(kFM == 2 || kFM % 4 == 0, "fragment slots");
@@ -517,56 +587,76 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
       for (int j = 0; j < kFN; ++j) vw[j][c] = s_scale[kScaled ? buf : 0][kScaled ? kBM + wn * kTN + j * 16 + i16 : 0][word];
     }
   };
+  // The compiler would move the reads back to their uses and the matrix
+  // instructions to a later block.  The wide kinds are left to it: there it
+  // overlaps the conversions with matrix instructions.
+  auto hold = [] {
+    if constexpr (!is_wide(kKind)) __builtin_amdgcn_sched_barrier(0);
+  };
+  auto issued = [](f32x4& v) {
+    if constexpr (!is_wide(kKind)) asm volatile("" : "+v"(v));
+  };
   auto step = [&](auto t, int ks) {
     constexpr int T = decltype(t)::value;
     constexpr int kBase = kFM == 2 ? 2 * (T & 1) : 0;          // slot of group 0
     constexpr int kNext = kFM == 2 ? 2 - 2 * (T & 1) : 0;      // slot of the next step's group 0
     typedef Prepared<kKind, T> Op;
-    const char* ta = smem + (ks & 1) * kStage + wm * kTM * kStep;
-    const char* na = smem + (1 - (ks & 1)) * kStage + wm * kTM * kStep;
-    const char* nw = smem + (1 - (ks & 1)) * kStage + (kBM + wn * kTN) * kStep;
+    const char* ta = smem + (ks & (kStages - 1)) * kStage + wm * kTM * kStep;
+    const char* na = smem + ((ks + 1) & (kStages - 1)) * kStage + wm * kTM * kStep;
+    const char* nw = smem + ((ks + 1) & (kStages - 1)) * kStage + (kBM + wn * kTN) * kStep;
     if constexpr (kScaled && T == 0) read_scales((ks >> 2) & 1);
     Op pw[kFN];
 #pragma unroll
     for (int j = 0; j < kFN; ++j) pw[j].set(fw[j], vw[j]);
 #pragma unroll
-    for (int i = 0; i < kFM - 2; ++i) {
-      if (kAhead == 1) fa[(kBase + i + 1) & 3] = read_frag(ta, (i + 1) * 16 + i16, g);
-      if (kAhead == 2 || i == kFM - 3) fa[(kBase + i + 2) & 3] = read_frag(ta, (i + 2) * 16 + i16, g);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < kFM - kAhead; ++i) {
+      fa[(kBase + i + kAhead) & 3] = read_frag(ta, (i + kAhead) * 16 + i16, g);
+      hold();
       Op pa;
       pa.set(fa[(kBase + i) & 3], va[i]);
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) acc[j][i] = mma<kKind, T>(pw[j], pa, acc[j][i]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int u = 0; u < kSubs<kKind>; ++u)
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) acc[j][i] = mma<kKind, T>(pw[j], pa, u, acc[j][i]);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) issued(acc[j][i]);
+      hold();
     }
     if constexpr (kScaled) {
       // the next four steps' scales: loaded a step before they go to LDS, which
       // is a step before they are read
-      if constexpr (T == 1) scale_next = load_scales(scale_row, 4 * (ks + 3), nblk);
-      if constexpr (T == 2) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_words(scale_next);
+      if constexpr (T == 1) scale_next = load_scales(scale_row, 4 * (step0 + ks + 3), nblk);
+      if constexpr (T == 2)
+        if (threadIdx.x < kBM + kBN) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_words(scale_next);
     }
-    step_barrier();                                            // this buffer is read, the other one filled
-    if (ks + 2 < steps) fetch(ks + 2);
-    Op pa[2];
-    pa[0].set(fa[(kBase + kFM - 2) & 3], va[kFM - 2]);
-    pa[1].set(fa[(kBase + kFM - 1) & 3], va[kFM - 1]);
+    // behind the barrier this buffer is read and the next one filled; copies that
+    // are on their way then are those of the steps from ks + 2 on
+    if (kStages > 2 && ks + kStages <= steps) step_barrier<(kStages - 2) * kLoads>();
+    else step_barrier<0>();
+    if (ks + kStages < steps) fetch(ks + kStages);
+    Op pa[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) pa[i].set(fa[(kBase + kFM - kAhead + i) & 3], va[kFM - kAhead + i]);
     // (after the last step these read an older one, unused)
     fa[kNext] = read_frag(na, i16, g);
     if (kAhead == 2) fa[kNext + 1] = read_frag(na, 16 + i16, g);
-    __builtin_amdgcn_sched_barrier(0);
+    hold();
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[j][kFM - 2 + i] = mma<kKind, T>(pw[j], pa[i], acc[j][kFM - 2 + i]);
+      for (int u = 0; u < kSubs<kKind>; ++u)
+#pragma unroll
+        for (int i = kFM - kAhead; i < kFM; ++i) acc[j][i] = mma<kKind, T>(pw[j], pa[i - kFM + kAhead], u, acc[j][i]);
+#pragma unroll
+      for (int i = kFM - kAhead; i < kFM; ++i) issued(acc[j][i]);
       fw[j] = read_frag(nw, j * 16 + i16, g);
-      __builtin_amdgcn_sched_barrier(0);
+      hold();
     }
   };
-  fetch(0);
-  if (steps > 1) fetch(1);
-  if constexpr (kScaled) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = scale_words(load_scales(scale_row, 0, nblk));
-  step_barrier();
+  for (int ks = 0; ks < kStages && ks < steps; ++ks) fetch(ks);
+  if constexpr (kScaled)
+    if (threadIdx.x < kBM + kBN) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = scale_words(load_scales(scale_row, 4 * step0, nblk));
+  step_barrier<0>();
 #pragma unroll
   for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + (kBM + wn * kTN) * kStep, j * 16 + i16, g);
   fa[0] = read_frag(smem + wm * kTM * kStep, i16, g);
@@ -588,7 +678,8 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   constexpr int kLd = kBN + 4;                                 // floats per row: 8 rows start on distinct banks
   constexpr int kRows = 32 * kWM;
   constexpr int kPer = kOutN / 8;                              // threads per row
-  static_assert(kRows * kLd * 4 <= 2 * kStage, "the pass fits the step buffers");
+  constexpr int kRowsPerIter = 64 * kWaves / kPer, kIters = kRows / kRowsPerIter;
+  static_assert(kRows * kLd * 4 <= kStages * kStage && kRows % kRowsPerIter == 0, "the pass fits the step buffers");
   float* tile = reinterpret_cast<float*>(smem);
   const int c = (int)(threadIdx.x % kPer) * 8;
   const int32_t n = n0 + c;
@@ -596,6 +687,12 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   cols.load(p, n);
 #pragma unroll 1
   for (int pass = 0; pass < kFM / 2; ++pass) {
+    Residual<8> res[kIters];
+#pragma unroll
+    for (int k = 0; k < kIters; ++k) {
+      const int r = (int)threadIdx.x / kPer + k * kRowsPerIter;
+      if (whole) res[k].load(p, min(m0 + (r / 32) * kTM + pass * 32 + r % 32, (int64_t)p.M - 1), n);
+    }
     lds_barrier();                                             // the steps' (or the last pass's) reads are done
     float* dst = tile + (wm * 32 + i16) * kLd + wn * kTN + 4 * g;
 #pragma unroll
@@ -607,8 +704,9 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
           for (int j = 0; j < kFN; ++j) *reinterpret_cast<f32x4*>(dst + i * 16 * kLd + j * 16) = acc[j][2 * q + i];
       }
     lds_barrier();
-#pragma unroll 1
-    for (int r = (int)threadIdx.x / kPer; r < kRows; r += 64 * kWaves / kPer) {
+#pragma unroll
+    for (int k = 0; k < kIters; ++k) {
+      const int r = (int)threadIdx.x / kPer + k * kRowsPerIter;
       const int64_t m = m0 + (r / 32) * kTM + pass * 32 + r % 32;
       const bool in = m < p.M && n < p.N;
       const int64_t mr = m < p.M ? m : (int64_t)p.M - 1;
@@ -623,8 +721,18 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
           u[4 * h + e] = y[e];
         }
       }
+      if (!whole) {
+        float* sum = p.partial + (((int64_t)(tile_no - p.whole) * p.parts + part) * kBM + (m - m0)) * kBN + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<f32x4*>(sum + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+          if constexpr (kGated)
+            *reinterpret_cast<f32x4*>(sum + kOutN + 4 * h) = f32x4{u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]};
+        }
+        continue;
+      }
       cols.finish(p, mr, v, u);
-      add_residual<8>(p, mr, n, v);
+      res[k].add(p, v);
       if (p.out_type != kOutBlock8) {
         if (in) store_run<8>(p, m, n, v);
       } else {
@@ -634,27 +742,70 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   }
 }
 
+// ---- joining the parts -----------------------------------------------------------
+// The sums of a tile's parts, added in order, through the same epilogue; a thread
+// finishes 8 consecutive outputs of a row.
+template <int kKind, bool kGated>
+__global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
+  const int32_t out_n = kGated ? bn / 2 : bn, per = out_n / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;   // bm * per is a multiple of 256
+  const int32_t c = (int32_t)(id % per) * 8;
+  const int32_t r = (int32_t)(id / per % bm);
+  const int32_t left = (int32_t)(id / ((int64_t)per * bm));
+  int32_t tm, tn;
+  tile_at(p, p.whole + left, tm, tn);
+  const int64_t m = (int64_t)tm * bm + r;
+  const int32_t n = tn * out_n + c;
+  const bool in = m < p.M && n < p.N;
+  const int64_t mr = m < p.M ? m : (int64_t)p.M - 1;
+  Columns<kKind, kGated, 8> cols;
+  cols.load(p, n);
+  Residual<8> res;
+  res.load(p, mr, n);
+  float v[8] = {}, u[8] = {};
+  const float* sum = p.partial + ((int64_t)left * p.parts * bm + r) * bn + c;
+  for (int32_t part = 0; part < p.parts; ++part, sum += (int64_t)bm * bn) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(sum + 4 * h);
+      const f32x4 y = *reinterpret_cast<const f32x4*>(sum + (kGated ? out_n : 0) + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[4 * h + e] += x[e];
+        u[4 * h + e] += y[e];
+      }
+    }
+  }
+  cols.finish(p, mr, v, u);
+  res.add(p, v);
+  if (p.out_type != kOutBlock8) {
+    if (in) store_run<8>(p, m, n, v);
+  } else {
+    store_block<8>(p, m, n, v, in);
+  }
+}
+
 // ---- few rows -------------------------------------------------------------------
-// At most 16 * kFM rows of a: bound by reading w once, so w goes straight from
-// memory to registers.  A workgroup owns kCols output columns (gated: their gate
-// and up rows); its wavefronts take the K steps in turn and their partial sums
-// are added in wavefront order through LDS.
-template <int kKind, int kFM, int kCols, int kWaves, bool kGated>
+// At most 16 rows of a: bound by reading w once, so w goes straight from memory to
+// registers.  A workgroup owns kCols output columns (gated: their gate and up
+// rows); its wavefronts take groups of four K steps in turn (a row's block scales
+// of a group are 16 bytes), kBatch steps' loads in flight at once, and their
+// partial sums are added in wavefront order through LDS.
+template <int kKind, int kCols, int kWaves, bool kGated>
 __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams p) {
   constexpr int kRows = kGated ? 2 * kCols : kCols;            // rows of w
   constexpr int kFN = kRows / 16;
+  // steps in flight: what 64 (16 wavefronts) or 128 kB of registers hold
+  constexpr int kBatch = kFN == 1 ? 4 : kFN == 2 ? (kWaves == 16 ? 2 : 4) : kWaves == 16 ? 1 : 2;
   constexpr int kLd = kRows + 4;                               // floats per row of a partial tile
-  __shared__ __align__(16) float part[kWaves][16 * kFM][kLd];
+  __shared__ __align__(16) float part[kWaves][16][kLd];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int32_t n0 = (int32_t)blockIdx.x * kCols;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * kFM);
   const int32_t nblk = p.kbytes / 32;
 
   const char* pw[kFN];
-  const char* pa[kFM];
   const uint8_t* sw[kFN];
-  const uint8_t* sa[kFM];
 #pragma unroll
   for (int j = 0; j < kFN; ++j) {
     const int r = j * 16 + i16;
@@ -664,83 +815,78 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
     pw[j] = p.w + row * p.ldw;
     sw[j] = static_cast<const uint8_t*>(p.w_scales) + row * nblk;
   }
+  const int64_t row = i16 < p.M ? i16 : p.M - 1;
+  const char* pa = p.a + row * p.lda;
+  const uint8_t* sa = static_cast<const uint8_t*>(p.a_scales) + row * nblk;
+  f32x4 acc[kFN];
 #pragma unroll
-  for (int i = 0; i < kFM; ++i) {
-    const int64_t m = m0 + i * 16 + i16;
-    const int64_t row = m < p.M ? m : (int64_t)p.M - 1;
-    pa[i] = p.a + row * p.lda;
-    sa[i] = static_cast<const uint8_t*>(p.a_scales) + row * nblk;
-  }
-  f32x4 acc[kFN][kFM];
-#pragma unroll
-  for (int j = 0; j < kFN; ++j)
-#pragma unroll
-    for (int i = 0; i < kFM; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < kFN; ++j) acc[j] = f32x4{0, 0, 0, 0};
 
   const int steps = (p.kbytes + kStep - 1) / kStep;
-  for (int ks = wave; ks < steps; ks += kWaves) {
-    // a chunk past the end of the rows counts as zeros
-    Frag fw[kFN], fa[kFM];
+  for (int first = 4 * wave; first < steps; first += 4 * kWaves) {
+    u32x4 da, dw[kFN];                                         // scales: word b, the blocks of step first + b
+    if constexpr (is_block8(kKind)) {
+      da = load_scales(sa, 4 * first, nblk);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int at = ks * kStep + (4 * c + g) * 16;
-      const bool in = at < p.kbytes;
-#pragma unroll
-      for (int j = 0; j < kFN; ++j) {
-        fw[j].c[c] = u32x4{0, 0, 0, 0};
-        if (in) fw[j].c[c] = *reinterpret_cast<const u32x4*>(pw[j] + at);
-      }
-#pragma unroll
-      for (int i = 0; i < kFM; ++i) {
-        fa[i].c[c] = u32x4{0, 0, 0, 0};
-        if (in) fa[i].c[c] = *reinterpret_cast<const u32x4*>(pa[i] + at);
-      }
-    }
-    // this step's scales of the blocks of chunks g and 4 + g (past the end the
-    // data are zeros: any scale does)
-    auto scales = [&](const uint8_t* row, uint32_t* d) {
-      d[0] = d[1] = kUnit;
-      if constexpr (is_block8(kKind)) {
-        d[0] = row[min(4 * ks + g / 2, nblk - 1)];
-        d[1] = row[min(4 * ks + 2 + g / 2, nblk - 1)];
-      }
-    };
-    Prepared<kKind, 0> qw[kFN], qa[kFM];
-    uint32_t sc[2];
-#pragma unroll
-    for (int j = 0; j < kFN; ++j) {
-      scales(sw[j], sc);
-      qw[j].set(fw[j], sc);
+      for (int j = 0; j < kFN; ++j) dw[j] = load_scales(sw[j], 4 * first, nblk);
     }
 #pragma unroll
-    for (int i = 0; i < kFM; ++i) {
-      scales(sa[i], sc);
-      qa[i].set(fa[i], sc);
+    for (int h = 0; h < 4; h += kBatch) {
+      // a chunk (or a step) past the end of the rows counts as zeros
+      Frag fw[kBatch][kFN], fa[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int at = (first + h + b) * kStep + (4 * c + g) * 16;
+          const bool in = at < p.kbytes;
+          fa[b].c[c] = u32x4{0, 0, 0, 0};
+          if (in) fa[b].c[c] = *reinterpret_cast<const u32x4*>(pa + at);
+#pragma unroll
+          for (int j = 0; j < kFN; ++j) {
+            fw[b][j].c[c] = u32x4{0, 0, 0, 0};
+            if (in) fw[b][j].c[c] = *reinterpret_cast<const u32x4*>(pw[j] + at);
+          }
+        }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        // the scales of the blocks of chunks g and 4 + g
+        auto pair = [&](const u32x4& d, uint32_t* v) {
+          v[0] = is_block8(kKind) ? d[h + b] >> (8 * (g / 2)) : kUnit;
+          v[1] = is_block8(kKind) ? d[h + b] >> (8 * (2 + g / 2)) : kUnit;
+        };
+        uint32_t v[2];
+        Prepared<kKind, 0> qa, qw[kFN];
+        pair(da, v);
+        qa.set(fa[b], v);
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) {
+          pair(dw[j], v);
+          qw[j].set(fw[b][j], v);
+        }
+#pragma unroll
+        for (int u = 0; u < kSubs<kKind>; ++u)
+#pragma unroll
+          for (int j = 0; j < kFN; ++j) acc[j] = mma<kKind, 0>(qw[j], qa, u, acc[j]);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < kFN; ++j)
-#pragma unroll
-      for (int i = 0; i < kFM; ++i) acc[j][i] = mma<kKind, 0>(qw[j], qa[i], acc[j][i]);
   }
 #pragma unroll
-  for (int j = 0; j < kFN; ++j)
-#pragma unroll
-    for (int i = 0; i < kFM; ++i)
-      *reinterpret_cast<f32x4*>(&part[wave][i * 16 + i16][j * 16 + 4 * g]) = acc[j][i];
+  for (int j = 0; j < kFN; ++j) *reinterpret_cast<f32x4*>(&part[wave][i16][j * 16 + 4 * g]) = acc[j];
   __syncthreads();
 
   // four outputs per thread: consecutive threads hold consecutive columns, so a
   // block of 32 columns is 8 neighbouring lanes
   constexpr int kQuads = kCols / 4;
-  for (int e = threadIdx.x; e < 16 * kFM * kQuads; e += 64 * kWaves) {
+  for (int e = threadIdx.x; e < 16 * kQuads; e += 64 * kWaves) {
     const int r = e / kQuads, c = (e % kQuads) * 4;
     f32x4 v = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < kWaves; ++w) {
       v += *reinterpret_cast<const f32x4*>(&part[w][r][c]);
       if constexpr (kGated) u += *reinterpret_cast<const f32x4*>(&part[w][r][kCols + c]);
     }
-    const int64_t m = m0 + r;
+    const int64_t m = r;
     const int32_t n = n0 + c;
     const bool in = m < p.M && n < p.N;
     float gv[4] = {v.x, v.y, v.z, v.w}, uv[4] = {u.x, u.y, u.z, u.w};
@@ -748,7 +894,9 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
     Columns<kKind, kGated, 4> cols;
     cols.load(p, n);
     cols.finish(p, mr, gv, uv);
-    add_residual<4>(p, mr, n, gv);
+    Residual<4> res;
+    res.load(p, mr, n);
+    res.add(p, gv);
     if (p.out_type != kOutBlock8) {
       if (in) store_run<4>(p, m, n, gv);
     } else if constexpr (kCols % 32 == 0) {
@@ -757,60 +905,133 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
   }
 }
 
-template <int kKind, int kBM, int kBN, int kWM, int kWN, bool kGated>
-hipError_t go_tile(LinParams p, hipStream_t stream) {
-  p.tiles_m = (p.M + kBM - 1) / kBM;
-  constexpr int kOutN = kGated ? kBN / 2 : kBN;
-  p.tiles_n = (p.N + kOutN - 1) / kOutN;
-  hipLaunchKernelGGL((linear_tile_kernel<kKind, kBM, kBN, kWM, kWN, kGated>), dim3((uint32_t)(p.tiles_m * p.tiles_n)),
-                     dim3(64 * kWM * kWN), 0, stream, p);
+// ---- choice of kernel and split -----------------------------------------------------
+enum { kFew, kTile64, kTile128, kTile256 };
+
+struct Plan {
+  int kernel;
+  int32_t tile, tiles_m, tiles_n;
+  int32_t whole, parts, part_steps;
+  size_t bytes;                                                // workspace
+};
+
+// What a launch takes, by measured rates in us: `step` per K step of a round (all
+// workgroups that the 256 CUs hold at once), `rest` per round (first copies and
+// epilogue).
+struct Rate { float step, rest; };
+
+Rate rate_of(int kind, int kernel) {
+  if (kernel == kTile256) return {kind == kBlock8 ? 2.0f : 1.7f, 11.0f};
+  if (kernel == kTile128) return {is_wide(kind) ? 1.5f : kind == kBlock8 ? 1.3f : 1.0f, 4.0f};
+  return {is_wide(kind) ? 0.8f : 0.42f, 2.0f};
+}
+
+// Tiles that fill whole rounds are computed whole.  Those of the last, partly
+// filled round may be cut along K into parts that fill it, at the price of a
+// second launch that joins the parts and of their sums' way to memory and back
+// (about 4 TB/s).
+Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) {
+  if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0};
+  const int32_t steps = (kbytes + kStep - 1) / kStep;
+  Plan best = {};
+  float best_cost = 0;
+  for (int kernel = kTile64; kernel <= (is_wide(kind) ? kTile128 : kTile256); ++kernel) {
+    const int32_t tile = kernel == kTile64 ? 64 : kernel == kTile128 ? 128 : 256;
+    const int32_t out_n = gated ? tile / 2 : tile;
+    const int32_t slots = kernel == kTile256 ? 256 : 512;
+    Plan q = {kernel, tile, (M + tile - 1) / tile, (N + out_n - 1) / out_n, 0, 1, steps, 0};
+    const int32_t total = q.tiles_m * q.tiles_n;
+    const Rate r = rate_of(kind, kernel);
+    const int32_t left = total % slots;
+    const float rounds = (float)(total / slots) * (steps * r.step + r.rest);
+    for (int32_t parts = 1; parts <= (left ? std::min(slots / left, 16) : 1); ++parts) {
+      // parts of whole groups of four steps (block scales come in fours)
+      int32_t each = parts == 1 ? steps : ((steps + parts - 1) / parts + 3) / 4 * 4;
+      const int32_t have = (steps + each - 1) / each;
+      if (have != parts) continue;
+      float cost = rounds;
+      if (left) cost += each * r.step + r.rest;
+      if (parts > 1) cost += 3.0f + (float)left * parts * tile * tile * 8.0f / 4e6f;
+      if (best_cost == 0 || cost < best_cost) {
+        best_cost = cost;
+        best = q;
+        best.parts = parts;
+        best.part_steps = each;
+        best.whole = parts > 1 ? total - left : total;
+        best.bytes = parts > 1 ? (size_t)left * parts * tile * tile * 4 : 0;
+      }
+    }
+  }
+  return best;
+}
+
+// 8-bit operands: the exact instructions where fp32's accuracy shows in the output
+// (fp32 itself; block scales, which change by a factor of two at a border) and where
+// reading w is the bound anyway.
+int kind_of(int kind, int32_t M, int32_t out_type) {
+  if (kind != kRow8 && kind != kBlock8) return kind;
+  if (M > 16 && out_type != kOutF32 && out_type != kOutBlock8) return kind;
+  return kind == kRow8 ? kRow8Wide : kBlock8Wide;
+}
+
+template <int kKind, int kTile, int kWM, int kWN, int kStages, bool kGated>
+hipError_t go_tile(const LinParams& p, hipStream_t stream) {
+  const int32_t left = p.tiles_m * p.tiles_n - p.whole;
+  hipLaunchKernelGGL((linear_tile_kernel<kKind, kTile, kTile, kWM, kWN, kStages, kGated>),
+                     dim3((uint32_t)(p.whole + left * p.parts)), dim3(64 * kWM * kWN), 0, stream, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || left == 0) return err;
+  const int32_t out_n = kGated ? kTile / 2 : kTile;
+  hipLaunchKernelGGL((linear_join_kernel<kKind, kGated>), dim3((uint32_t)(left * (kTile * (out_n / 8) / 256))), dim3(256), 0,
+                     stream, p, kTile, kTile);
   return hipGetLastError();
 }
 
-template <int kKind, int kFM, int kCols, bool kGated>
-hipError_t go_few(LinParams p, hipStream_t stream) {
-  constexpr int kWaves = 8;
-  hipLaunchKernelGGL((linear_few_kernel<kKind, kFM, kCols, kWaves, kGated>),
-                     dim3((uint32_t)((p.N + kCols - 1) / kCols), (uint32_t)((p.M + 16 * kFM - 1) / (16 * kFM))),
-                     dim3(64 * kWaves), 0, stream, p);
+template <int kKind, int kCols, bool kGated>
+hipError_t go_few(const LinParams& p, hipStream_t stream) {
+  const uint32_t blocks = (uint32_t)((p.N + kCols - 1) / kCols);
+  // up to a workgroup per CU: 16 wavefronts, where there are steps for them
+  if (blocks <= 256 && p.kbytes > 32 * kStep)
+    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 16, kGated>), dim3(blocks), dim3(1024), 0, stream, p);
+  else
+    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 8, kGated>), dim3(blocks), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 
 template <int kKind, bool kGated>
-hipError_t go(const LinParams& p, hipStream_t stream) {
-  if (p.M <= 64) {
-    // bound by reading w: 8-bit operands take the exact instruction whatever the output
-    constexpr int kFew = kKind == kRow8 ? kRow8Wide : kKind == kBlock8 ? kBlock8Wide : kKind;
-    if constexpr (kFew == kKind) {
-      if (p.M <= 16) return p.out_type == kOutBlock8 ? go_few<kKind, 1, 32, kGated>(p, stream) : go_few<kKind, 1, 16, kGated>(p, stream);
-      return p.out_type == kOutBlock8 ? go_few<kKind, 2, 32, kGated>(p, stream) : go_few<kKind, 2, 16, kGated>(p, stream);
-    } else {
-      return go<kFew, kGated>(p, stream);
-    }
-  }
-  if constexpr (kKind == kRow8 || kKind == kBlock8)
-    if (p.out_type == kOutF32 || p.out_type == kOutBlock8) return go<kKind == kRow8 ? kRow8Wide : kBlock8Wide, kGated>(p, stream);
-  const int64_t cols = kGated ? 2 * (int64_t)p.N : p.N;
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm) * ((cols + bn - 1) / bn); };
+hipError_t go(LinParams p, void* workspace, hipStream_t stream) {
+  const Plan plan = plan_of(p.M, p.N, p.kbytes, kKind, kGated);
+  if constexpr (kKind != kRow8 && kKind != kBlock8)
+    if (plan.kernel == kFew)
+      return p.out_type == kOutBlock8 ? go_few<kKind, 32, kGated>(p, stream) : go_few<kKind, 16, kGated>(p, stream);
+  p.tiles_m = plan.tiles_m;
+  p.tiles_n = plan.tiles_n;
+  p.whole = plan.whole;
+  p.parts = plan.parts;
+  p.part_steps = plan.part_steps;
+  p.partial = static_cast<float*>(workspace);
   if constexpr (!is_wide(kKind))
-    if (tiles(256, 256) >= 192) return go_tile<kKind, 256, 256, 2, 4, kGated>(p, stream);
-  if (tiles(128, 128) >= 192) return go_tile<kKind, 128, 128, 2, 2, kGated>(p, stream);
-  return go_tile<kKind, 64, 64, 2, 1, kGated>(p, stream);
+    if (plan.kernel == kTile256) return go_tile<kKind, 256, 2, 4, 2, kGated>(p, stream);
+  if (plan.kernel == kTile128) return go_tile<kKind, 128, 2, 2, 2, kGated>(p, stream);
+  return go_tile<kKind, 64, 2, 2, 4, kGated>(p, stream);
 }
 
 template <int kKind>
-hipError_t go_gated(const LinParams& p, int32_t gated, hipStream_t stream) {
-  return gated ? go<kKind, true>(p, stream) : go<kKind, false>(p, stream);
+hipError_t go_gated(const LinParams& p, int32_t gated, void* workspace, hipStream_t stream) {
+  return gated ? go<kKind, true>(p, workspace, stream) : go<kKind, false>(p, workspace, stream);
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t linear_workspace_bytes(const LinearArgs& a) {
+  if (a.M == 0 || a.N == 0) return 0;
+  return plan_of(a.M, a.N, a.K * (a.kind <= kF16 ? 2 : 1), kind_of(a.kind, a.M, a.out_type), a.gated != 0).bytes;
+}
 
-hipError_t launch_linear(const LinearArgs& a, void*, hipStream_t stream) {
+hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int32_t esz = a.kind <= kF16 ? 2 : 1;
-  LinParams p;
+  LinParams p = {};
   p.a = static_cast<const char*>(a.a);
   p.w = static_cast<const char*>(a.w);
   p.a_scales = a.a_scales;
@@ -825,11 +1046,13 @@ hipError_t launch_linear(const LinearArgs& a, void*, hipStream_t stream) {
   p.ldo = a.ldo;
   p.M = a.M; p.N = a.N; p.kbytes = a.K * esz;
   p.act = a.act; p.bias_type = a.bias_type; p.residual_type = a.residual_type; p.out_type = a.out_type;
-  switch (a.kind) {
-    case kBf16: return go_gated<kBf16>(p, a.gated, stream);
-    case kF16: return go_gated<kF16>(p, a.gated, stream);
-    case kRow8: return go_gated<kRow8>(p, a.gated, stream);
-    case kBlock8: return go_gated<kBlock8>(p, a.gated, stream);
+  switch (kind_of(a.kind, a.M, a.out_type)) {
+    case kBf16: return go_gated<kBf16>(p, a.gated, workspace, stream);
+    case kF16: return go_gated<kF16>(p, a.gated, workspace, stream);
+    case kRow8: return go_gated<kRow8>(p, a.gated, workspace, stream);
+    case kBlock8: return go_gated<kBlock8>(p, a.gated, workspace, stream);
+    case kRow8Wide: return go_gated<kRow8Wide>(p, a.gated, workspace, stream);
+    case kBlock8Wide: return go_gated<kBlock8Wide>(p, a.gated, workspace, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -20,6 +20,7 @@ graph.  Forward only: no gradients are recorded.
 from __future__ import annotations
 
 import contextlib
+import functools
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -117,20 +118,38 @@ def _check_apart(out, name, others, same_ok=False):
 
 _HERE = contextlib.nullcontext()
 
+# A small call costs the host more than the GPU (about 10 us against 3), so what
+# every call does goes the short way: the current stream's handle, the current
+# device and new tensors by torch's own C functions (0.1, 0.1 and 0.8 us where
+# current_stream().cuda_stream, current_device() and new_empty take 1.9, 0.3 and
+# 1.5), and no message is formed unless it is raised.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+try:
+    _empty_strided = torch._C._dynamo.guards._empty_strided_cuda       # on the current device
+except AttributeError:
+    def _empty_strided(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _empty(rows, cols, dtype):
+    return _empty_strided((rows, cols), (cols, 1), dtype)
+
 
 def _on(tensors, stream):
     """(stream handle, context) of a call: checks that its tensors share a GPU;
     inside the context that device and `stream` are current, so outputs are
     allocated there.  Tensors of another stream are marked as used on this one."""
-    dev = tensors[0].device
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors of one call must be on one device: {t.device} and {dev}")
-    _need(dev.type == "cuda", f"tensors must be on a GPU, not on {dev}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors of one call must be on one device: {t.device} and {tensors[0].device}")
+    if index < 0 or not tensors[0].is_cuda:
+        raise ValueError(f"tensors must be on a GPU, not on {tensors[0].device}")
     if stream is None:
-        # (the public current_stream(dev).cuda_stream is this, behind 2 us of object building)
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-        return handle, _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+        return _raw_stream(index), _HERE if _current_device() == index else torch.cuda.device(index)
+    dev = tensors[0].device
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
     _need(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
@@ -141,20 +160,23 @@ def _on(tensors, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)       # makes its device current, too
 
 
-def _fp8_out(rows, K, scales, like):
-    codes = like.new_empty((rows, K), dtype=torch.uint8)
+def _fp8_out(rows, K, scales):
+    codes = _empty(rows, K, torch.uint8)
     if scales == "row":
-        return FP8Rows(codes, like.new_empty((rows,), dtype=torch.float32))
-    return FP8Rows(codes, like.new_empty((rows, K // 32), dtype=torch.uint8))
+        return FP8Rows(codes, _empty_strided((rows,), (1,), torch.float32))
+    return FP8Rows(codes, _empty(rows, K // 32, torch.uint8))
 
 
 def _check_K(K):
-    _need(8 <= K <= 32768 and K % 8 == 0, f"K must be a multiple of 8 in [8, 32768], not {K}")
+    if not (8 <= K <= 32768 and K % 8 == 0):
+        raise ValueError(f"K must be a multiple of 8 in [8, 32768], not {K}")
 
 
 def _check_scales(scales, K):
-    _need(isinstance(scales, str) and scales in _FP8, 'scales must be "row" or "mx"')
-    _need(scales != "mx" or K % 32 == 0, f'"mx" scales need a multiple of 32 columns, not {K}')
+    if not (isinstance(scales, str) and scales in _FP8):
+        raise ValueError('scales must be "row" or "mx"')
+    if scales == "mx" and K % 32:
+        raise ValueError(f'"mx" scales need a multiple of 32 columns, not {K}')
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
@@ -177,9 +199,9 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     if residual is not None:
         ldr = _rows(residual, "residual", K, T, (dtype,))
     if weight is not None:
-        _need(isinstance(weight, torch.Tensor) and weight.dtype == dtype and
-              weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0,
-              f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
+        if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and
+                weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0):
+            raise ValueError(f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
     if scales is not None:
         _check_scales(scales, K)
     _need(want_y or out is None, "out needs want_y")
@@ -204,13 +226,13 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     with ctx:
         y = total = fp8 = codes = sc = None
         if want_y:
-            y = x.new_empty((T, K)) if out is None else out
+            y = _empty(T, K, dtype) if out is None else out
         if residual is not None:
-            total = x.new_empty((T, K)) if total_out is None else total_out
+            total = _empty(T, K, dtype) if total_out is None else total_out
         kind = _lib.FP8_NONE
         if scales is not None:
             kind = _FP8[scales]
-            fp8 = codes, sc = _fp8_out(T, K, scales, x)
+            fp8 = codes, sc = _fp8_out(T, K, scales)
         _lib.rmsnorm(_TYPES[dtype], x, ldx, residual, ldr, weight, weight_offset, eps, T, K,
                      total, lds, y, ldy, kind, codes, sc, handle)
     return NormOut(y, total, fp8)
@@ -226,7 +248,7 @@ def quantize_fp8(x: torch.Tensor, scales: str = "mx", *, stream=None) -> FP8Rows
     _check_scales(scales, K)
     handle, ctx = _on((x,), stream)
     with ctx:
-        fp8 = _fp8_out(T, K, scales, x)
+        fp8 = _fp8_out(T, K, scales)
         _lib.quantize_rows_fp8(_TYPES[x.dtype], x, ldx, T, K, _FP8[scales], fp8.codes, fp8.scales,
                                handle)
     return fp8
@@ -243,20 +265,22 @@ def _operand(v, name):
         step, kind = 8, _TYPES[v.dtype]
         K = v.shape[1]
     else:
-        _need(isinstance(v, tuple) and len(v) == 2,
-              f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
+        if not (isinstance(v, tuple) and len(v) == 2):
+            raise ValueError(f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
         v, scales = v
         ld = _rows(v, name, dtypes=_BYTES)
         rows, K = v.shape
-        _need(isinstance(scales, torch.Tensor) and scales.is_contiguous(),
-              f"{name}'s scales must be a contiguous tensor")
+        if not (isinstance(scales, torch.Tensor) and scales.is_contiguous()):
+            raise ValueError(f"{name}'s scales must be a contiguous tensor")
         if scales.dtype == torch.float32:
             step, kind, shape = 16, _lib.TYPE_FP8_ROW, (rows,)
         else:
             step, kind, shape = 32, _lib.TYPE_FP8_MX, (rows, K // 32)
-            _need(scales.dtype == torch.uint8, f"{name}'s scales must be fp32 or uint8")
-        _need(scales.shape == shape, f"{name}'s scales must be of shape {shape}")
-    _need(K >= step and K % step == 0, f"{name} must have a multiple of {step} columns, not {K}")
+            _need(scales.dtype == torch.uint8, "block scales must be uint8, row scales fp32")
+        if scales.shape != shape:
+            raise ValueError(f"{name}'s scales must be of shape {shape}")
+    if K < step or K % step:
+        raise ValueError(f"{name} must have a multiple of {step} columns, not {K}")
     return kind, v, ld, scales
 
 
@@ -273,6 +297,12 @@ def _plain(t, name, shape, dtypes=_FLOATS):
                 return max(ld, shape[1])
     raise ValueError(f"{name} must be a {'/'.join(str(d).replace('torch.', '') for d in dtypes)} "
                      f"{list(shape)} tensor with contiguous rows")
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(M, N, K, kind, out_type, gated):
+    return _lib.linear_workspace_size(
+        _lib.Linear(M=M, N=N, K=K, type=kind, out_type=out_type, gated=gated))
 
 
 def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
@@ -295,7 +325,8 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     _need(kind == wkind, "a and w must be of one type, with one kind of scales")
     M, K = av.shape
     rows = wv.shape[0]
-    _need(wv.shape[1] == K, f"w must have {K} columns, as a")
+    if wv.shape[1] != K:
+        raise ValueError(f"w must have {K} columns, as a")
     _need(gated is False or gated is True, "gated must be True or False")
     _need(not gated or rows % 2 == 0, "a gated w has an even number of rows")
     N = rows // 2 if gated else rows
@@ -313,8 +344,9 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     mx = isinstance(out_dtype, str)
     ldo = N
     if mx:
-        _need(out_dtype == "mx", f'out_dtype must be bf16, fp16, fp32 or "mx", not {out_dtype!r}')
-        _need(N % 32 == 0, f'an "mx" result needs a multiple of 32 columns, not {N}')
+        _need(out_dtype == "mx", 'out_dtype must be bf16, fp16, fp32 or "mx"')
+        if N % 32:
+            raise ValueError(f'an "mx" result needs a multiple of 32 columns, not {N}')
         _need(out is None, 'out is not taken with out_dtype "mx"')
         out_type = _lib.TYPE_FP8_MX
     else:
@@ -322,7 +354,7 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
             out_dtype = out.dtype if isinstance(out, torch.Tensor) else \
                 torch.bfloat16 if a_sc is not None else av.dtype
         out_type = _TYPES.get(out_dtype)
-        _need(out_type is not None, f'out_dtype must be bf16, fp16, fp32 or "mx", not {out_dtype}')
+        _need(out_type is not None, 'out_dtype must be bf16, fp16, fp32 or "mx"')
         if out is not None:
             ldo = _plain(out, "out", (M, N), (out_dtype,))
             _check_apart(out, "out", (av, wv, a_sc, w_sc, bias))
@@ -331,16 +363,16 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     with ctx:
         out_scales = None
         if mx:
-            res, out_scales = _fp8_out(M, N, "mx", av)
+            res, out_scales = _fp8_out(M, N, "mx")
         else:
-            res = av.new_empty((M, N), dtype=out_dtype) if out is None else out
+            res = _empty(M, N, out_dtype) if out is None else out
         p = _lib.Linear(
             av.data_ptr(), None if a_sc is None else a_sc.data_ptr(), wv.data_ptr(),
             None if w_sc is None else w_sc.data_ptr(), None if bias is None else bias.data_ptr(),
             None if residual is None else residual.data_ptr(), res.data_ptr(),
             None if out_scales is None else out_scales.data_ptr(), lda, ldw, ldr, ldo, M, N, K,
             kind, bias_type, res_type, out_type, act_id, gated)
-        n = _lib.linear_workspace_size(p)
-        ws = av.new_empty((n,), dtype=torch.uint8) if n else None
+        n = _workspace_bytes(M, N, K, kind, out_type, gated)
+        ws = _empty_strided((n,), (1,), torch.uint8) if n else None
         _lib.linear(p, ws, n, handle)
     return FP8Rows(res, out_scales) if mx else res

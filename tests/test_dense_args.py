@@ -188,7 +188,7 @@ def test_c_linear_checks():
                dict(ldo=40), dict(out_type=L.TYPE_FP32, out=GOOD + 2), dict(out_type=L.TYPE_BF16, out=GOOD + 1)):
         assert c_linear(**kw) == L.ERR_INVALID_ARG, kw
     for kw in (dict(K=(1 << 24) + 32, lda=1 << 26, ldw=1 << 26), dict(N=(1 << 24) + 32, ldo=1 << 26, ldr=1 << 26),
-               dict(M=1 << 30, N=1 << 20, ldo=1 << 20, ldr=1 << 20)):
+               dict(M=1 << 30, N=1 << 20, ldo=1 << 20, ldr=1 << 20), dict(lda=(1 << 23) + 16), dict(ldw=(1 << 23) + 16)):
         assert c_linear(**kw) == L.ERR_UNSUPPORTED, kw
 
 
