@@ -630,7 +630,7 @@ typedef enum {
  * out may be residual itself (same pointer, type and stride); it must not
  * overlap any input in another way.  M == 0 or N == 0 is a no-op.  K <= 2^22,
  * N <= 2^24, row strides of a and w <= 2^23 bytes and ceil(M / 256) *
- * ceil(N' / 256) <= 2^22 with N' the rows of w, else NVFP4_ERR_UNSUPPORTED.
+ * ceil(N' / 256) <= 2^20 with N' the rows of w, else NVFP4_ERR_UNSUPPORTED.
  */
 typedef struct {
   const void* a;

@@ -47,7 +47,7 @@ nvfp4_status_t check_linear_sizes(const nvfp4_linear_t* p, LinearArgs* a) {
   // 32-bit sizes inside the kernels: a tile's offsets, rows of w, tiles of a launch
   if (p->K > (1 << 22) || p->N > (1 << 24)) return NVFP4_ERR_UNSUPPORTED;
   const int64_t tiles = (((int64_t)p->M + 255) / 256) * (((int64_t)p->N * (p->gated + 1) + 255) / 256);
-  if (tiles > (1 << 22)) return NVFP4_ERR_UNSUPPORTED;
+  if (tiles > (1 << 20)) return NVFP4_ERR_UNSUPPORTED;
   a->M = p->M; a->N = p->N; a->K = p->K;
   a->kind = p->type == NVFP4_TYPE_BF16 ? 0 : p->type == NVFP4_TYPE_FP16 ? 1 : p->type == NVFP4_TYPE_FP8_ROW ? 2 : 3;
   a->act = p->act; a->gated = p->gated;

@@ -1,5 +1,7 @@
 """GPU tests of the dense operators (rms_norm, quantize_fp8, linear) against
-the float64 oracle, with tolerances derived there; bit-exact for the quantiser."""
+the float64 oracle, with tolerances derived there; bit-exact for the quantiser.
+Covered besides the values: strides and guards, NaN and infinities, offsets past
+32 bits, streams, graph replays, and the operators around a routed-expert layer."""
 import itertools
 
 import numpy as np
@@ -309,6 +311,25 @@ def test_linear_large(M, N, K, kind, gated, out):
     linear_case(M, N, K, kind, "gelu_tanh" if gated else None, gated, F32, None if out == "mx" else BF16, out, seed=M)
 
 
+def workspace(M, N, K, kind, out, gated):
+    from nvfp4_w4a4_expert_amd import _lib as L
+    types = {"bf16": L.TYPE_BF16, "fp16": L.TYPE_FP16, "row": L.TYPE_FP8_ROW, "mx": L.TYPE_FP8_MX}
+    outs = {BF16: L.TYPE_BF16, F16: L.TYPE_FP16, F32: L.TYPE_FP32, "mx": L.TYPE_FP8_MX}
+    return L.linear_workspace_size(L.Linear(M=M, N=N, K=K, type=types[kind], out_type=outs[out], gated=gated))
+
+
+# sizes whose last round is cut along K: all of the tiles or the last ones, parts of
+# equal and of unequal length, a ragged last step, every kind of output
+@pytest.mark.parametrize("M,N,K,kind,gated,out", [
+    (17, 130, 2816, "bf16", False, F32), (17, 31, 2808, "fp16", True, F16), (48, 128, 2816, "bf16", False, F32),
+    (40, 96, 2848, "mx", True, "mx"), (64, 320, 5632, "mx", False, BF16), (33, 77, 2832, "row", False, F32),
+    (65, 128, 4224, "row", False, "mx"), (300, 127, 2816, "bf16", True, BF16), (130, 64, 8192, "mx", False, F32),
+    (2300, 130, 2112, "bf16", False, BF16), (4100, 2112, 1416, "bf16", True, BF16), (4096, 2112, 2816, "mx", True, "mx")])
+def test_linear_cut_along_k(M, N, K, kind, gated, out):
+    assert workspace(M, N, K, kind, out, gated) > 0
+    linear_case(M, N, K, kind, "gelu_tanh" if gated else "silu", gated, BF16, F32 if out == F32 else BF16, out, seed=N)
+
+
 @pytest.mark.parametrize("M", [3, 40, 100, 300])
 @pytest.mark.parametrize("kind", KINDS)
 def test_linear_strides_edges_and_guards(M, kind):
@@ -361,6 +382,29 @@ def test_linear_nan_and_inf_stay_in_their_rows(kind):
         OD.check_rounded(f64(got)[~bad.numpy()], ref[~bad.numpy()], err[~bad.numpy()], F32)
 
 
+def test_offsets_past_32_bits():
+    """Rows beyond 2^31 elements and 2^32 bytes of an operand, the residual and the
+    result: the last rows are those of a call on them alone."""
+    M, N, K = 70100, 32768, 64
+    a, w = rand((M, K), 35).cuda(), rand((N, K), 36, scale=0.1).cuda()
+    res = torch.ones((M, N), dtype=BF16, device="cuda")
+    got = D().linear(a, w, residual=res, out=res)
+    for lo, hi in ((0, 300), (M - 300, M)):
+        ref, err = OD.linear(f64(a[lo:hi]), f64(w[:512]), residual=1.0)
+        OD.check_rounded(f64(got[lo:hi, :512]), ref, err, BF16)
+        ref, err = OD.linear(f64(a[lo:hi]), f64(w[-512:]), residual=1.0)
+        OD.check_rounded(f64(got[lo:hi, -512:]), ref, err, BF16)
+    # the same buffer as norm input, in place, and as an operand of many rows
+    tail = got[-3:].clone()
+    n = D().rms_norm(got, out=got, scales="mx")
+    y, err = OD.rms_norm(f64(tail), None, 1e-6, 0.0)
+    OD.check_rounded(f64(got[-3:]), y, err, BF16)
+    OD.check_fp8(n.fp8.codes[-3:].cpu().numpy(), n.fp8.scales[-3:].cpu().numpy(), y, err)
+    out = D().linear(got, rand((16, N), 37, scale=0.01).cuda(), out_dtype=F32)
+    ref, err = OD.linear(f64(got[-3:]), f64(rand((16, N), 37, scale=0.01)))
+    OD.check_rounded(f64(out[-3:]), ref, err, F32)
+
+
 def test_linear_empty():
     w = rand((24, 64), 41).cuda()
     assert D().linear(rand((0, 64), 40).cuda(), w).shape == (0, 24)
@@ -387,9 +431,12 @@ def chain_inputs(T, seed, H=256, I=160, E=24):
     return x, h, wn, wr, wgu, wd
 
 
-@pytest.mark.parametrize("T", [1, 16, 70, 400])
-def test_chain_stage_by_stage(T):
-    x, h, wn, wr, wgu, wd = chain_inputs(T, 50)
+SMALL, MODEL = dict(H=256, I=160, E=24), dict(H=2816, I=704, E=128)       # MODEL's products are cut along K
+
+
+@pytest.mark.parametrize("T,sizes", [(1, SMALL), (16, SMALL), (70, SMALL), (400, SMALL), (16, MODEL), (33, MODEL), (260, MODEL)])
+def test_chain_stage_by_stage(T, sizes):
+    x, h, wn, wr, wgu, wd = chain_inputs(T, 50, **sizes)
     n, logits, a, out = chain(x, h, wn, wr, wgu, wd)
     s = (x.float() + h.float()).to(BF16)
     assert torch.equal(n.total, s)
@@ -412,9 +459,9 @@ def same(p, q):
         torch.equal(p[2].codes, q[2].codes) and torch.equal(p[2].scales, q[2].scales) and torch.equal(p[3], q[3])
 
 
-@pytest.mark.parametrize("T", [4, 300])
-def test_two_streams_and_repeats(T):
-    one, two = chain_inputs(T, 60), chain_inputs(T, 70)
+@pytest.mark.parametrize("T,sizes", [(4, SMALL), (300, SMALL), (20, MODEL), (150, MODEL)])
+def test_two_streams_and_repeats(T, sizes):
+    one, two = chain_inputs(T, 60, **sizes), chain_inputs(T, 70, **sizes)
     want = chain(*one), chain(*two)
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -443,9 +490,9 @@ def test_stream_argument(raw):
     assert torch.equal(want[1], got[1]) and torch.equal(want[2].codes, got[2].codes)
 
 
-@pytest.mark.parametrize("T", [3, 290])
-def test_graph_replays(T):
-    args = chain_inputs(T, 90)
+@pytest.mark.parametrize("T,sizes", [(3, SMALL), (290, SMALL), (20, MODEL), (150, MODEL)])
+def test_graph_replays(T, sizes):
+    args = chain_inputs(T, 90, **sizes)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -455,7 +502,7 @@ def test_graph_replays(T):
     with torch.cuda.graph(graph):
         got = chain(*args)
     for k in range(5):
-        fresh = chain_inputs(T, 100 + k)
+        fresh = chain_inputs(T, 100 + k, **sizes)
         args[0].copy_(fresh[0])
         args[1].copy_(fresh[1])
         graph.replay()
@@ -466,7 +513,7 @@ def test_graph_replays(T):
 
 def test_two_graphs_share_nothing():
     """Two captured calls with a workspace each, replayed on two streams at once."""
-    one, two = chain_inputs(20, 110), chain_inputs(20, 120)
+    one, two = chain_inputs(20, 110, **MODEL), chain_inputs(20, 120, **MODEL)
     want = chain(*one), chain(*two)
     graphs, outs = [], []
     for args in (one, two):
