@@ -297,18 +297,21 @@ def moe_forward_noalloc(weights: MoEWeights, x, router_logits, num_tokens: int, 
                                           _stream(stream)), "nvfp4_moe_forward_noalloc")
 
 
-def rmsnorm(type, x, ldx: int, residual, ldr: int, weight, weight_offset: float, eps: float,
-            num_rows: int, K: int, sum_out, lds: int, y_out, ldy: int, fp8: int, codes, scales,
-            stream=None):
-    _check(_lib.nvfp4_rmsnorm(type, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), weight_offset,
-                              eps, num_rows, K, _ptr(sum_out), lds, _ptr(y_out), ldy, fp8,
-                              _ptr(codes), _ptr(scales), _stream(stream)), "nvfp4_rmsnorm")
+# The dense operators: pointers are addresses (integers, None for NULL) and the
+# stream is a handle, so that a small call pays for no more than the C call.
+
+def rmsnorm(*args):
+    """The arguments of nvfp4_rmsnorm, in order."""
+    status = _lib.nvfp4_rmsnorm(*args)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_rmsnorm")
 
 
-def quantize_rows_fp8(type, x, ldx: int, num_rows: int, K: int, fp8: int, codes, scales,
-                      stream=None):
-    _check(_lib.nvfp4_quantize_rows_fp8(type, _ptr(x), ldx, num_rows, K, fp8, _ptr(codes),
-                                        _ptr(scales), _stream(stream)), "nvfp4_quantize_rows_fp8")
+def quantize_rows_fp8(*args):
+    """The arguments of nvfp4_quantize_rows_fp8, in order."""
+    status = _lib.nvfp4_quantize_rows_fp8(*args)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_quantize_rows_fp8")
 
 
 def linear_workspace_size(p: Linear) -> int:
@@ -318,6 +321,7 @@ def linear_workspace_size(p: Linear) -> int:
     return n.value
 
 
-def linear(p: Linear, workspace, workspace_bytes: int, stream=None):
-    _check(_lib.nvfp4_linear(ctypes.byref(p), _ptr(workspace), workspace_bytes, _stream(stream)),
-           "nvfp4_linear")
+def linear(p: Linear, workspace, workspace_bytes: int, stream):
+    status = _lib.nvfp4_linear(ctypes.byref(p), workspace, workspace_bytes, stream)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_linear")

@@ -68,8 +68,9 @@ def _need(ok, msg):
 
 
 def _rows(t, name, K=None, rows=None, dtypes=_HALF):
-    """The row stride of a 2-D tensor whose rows are contiguous and start on
-    16-byte boundaries (of one row, whose stride is arbitrary: K rounded up)."""
+    """(rows, K, row stride, address) of a 2-D tensor whose rows are contiguous
+    and start on 16-byte boundaries (the stride of one row, which is arbitrary,
+    as if it were followed by another)."""
     shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes else ()
     if len(shape) != 2 or (K is not None and shape[1] != K) or (rows is not None and shape[0] != rows):
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
@@ -80,9 +81,10 @@ def _rows(t, name, K=None, rows=None, dtypes=_HALF):
     ld, step = t.stride()
     if T <= 1:
         ld = -(-K // per16) * per16
-    if T and K and (ld < K or ld % per16 or (step != 1 and K != 1) or t.data_ptr() % 16):
+    at = t.data_ptr()
+    if (ld < K or ld % per16 or (step != 1 and K != 1) or at % 16) and T and K:
         raise ValueError(f"{name}'s rows must be contiguous and start on 16-byte boundaries")
-    return ld
+    return T, K, ld, at
 
 
 def _span(t):
@@ -192,65 +194,67 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     total, fp8): y of x's type (want_y, or into `out`); total = s, given with a
     residual (into `total_out`, which like `out` may be x or residual); fp8 the
     8-bit rows when `scales` is "row" or "mx", rounded from the fp32 values."""
-    ldx = _rows(x, "x")
-    T, K = x.shape
+    T, K, ldx, x_at = _rows(x, "x")
     _check_K(K)
-    dtype, ldr, lds = x.dtype, 0, 0
+    dtype = x.dtype
+    r_at = w_at = y_at = total_at = codes_at = scales_at = None
+    ldr = lds = 0
+    ldy = K
     if residual is not None:
-        ldr = _rows(residual, "residual", K, T, (dtype,))
+        _, _, ldr, r_at = _rows(residual, "residual", K, T, (dtype,))
+    elif total_out is not None:
+        raise ValueError("total_out needs a residual")
+    elif not want_y and scales is None:
+        raise ValueError("nothing is asked for: want_y, scales or a residual")
     if weight is not None:
         if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and
                 weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0):
             raise ValueError(f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
+        w_at = weight.data_ptr()
     if scales is not None:
         _check_scales(scales, K)
-    _need(want_y or out is None, "out needs want_y")
-    _need(residual is not None or total_out is None, "total_out needs a residual")
-    _need(want_y or scales is not None or residual is not None,
-          "nothing is asked for: want_y, scales or a residual")
     eps, weight_offset = float(eps), float(weight_offset)
-    _need(0.0 <= eps < 3.4e38 and abs(weight_offset) < 3.4e38,
-          "eps must be finite and >= 0, weight_offset finite")
-    ldy = K
+    if not (0.0 <= eps < 3.4e38 and -3.4e38 < weight_offset < 3.4e38):
+        raise ValueError("eps must be finite and >= 0, weight_offset finite")
     if out is not None:
-        ldy = _rows(out, "out", K, T, (dtype,))
+        _need(want_y, "out needs want_y")
+        _, _, ldy, y_at = _rows(out, "out", K, T, (dtype,))
         _check_apart(out, "out", (weight, total_out))
         _check_apart(out, "out", (x, residual), True)
-    if residual is not None:
-        lds = K
-        if total_out is not None:
-            lds = _rows(total_out, "total_out", K, T, (dtype,))
-            _check_apart(total_out, "total_out", (weight,))
-            _check_apart(total_out, "total_out", (x, residual), True)
+    if total_out is not None:
+        _, _, lds, total_at = _rows(total_out, "total_out", K, T, (dtype,))
+        _check_apart(total_out, "total_out", (weight,))
+        _check_apart(total_out, "total_out", (x, residual), True)
     handle, ctx = _on((x, residual, weight, out, total_out), stream)
     with ctx:
-        y = total = fp8 = codes = sc = None
-        if want_y:
-            y = _empty(T, K, dtype) if out is None else out
-        if residual is not None:
-            total = _empty(T, K, dtype) if total_out is None else total_out
-        kind = _lib.FP8_NONE
+        fp8, kind = None, _lib.FP8_NONE
+        if want_y and out is None:
+            out = _empty(T, K, dtype)
+            y_at = out.data_ptr()
+        if residual is not None and total_out is None:
+            total_out, lds = _empty(T, K, dtype), K
+            total_at = total_out.data_ptr()
         if scales is not None:
             kind = _FP8[scales]
-            fp8 = codes, sc = _fp8_out(T, K, scales)
-        _lib.rmsnorm(_TYPES[dtype], x, ldx, residual, ldr, weight, weight_offset, eps, T, K,
-                     total, lds, y, ldy, kind, codes, sc, handle)
-    return NormOut(y, total, fp8)
+            fp8 = _fp8_out(T, K, scales)
+            codes_at, scales_at = fp8.codes.data_ptr(), fp8.scales.data_ptr()
+        _lib.rmsnorm(_TYPES[dtype], x_at, ldx, r_at, ldr, w_at, weight_offset, eps, T, K,
+                     total_at, lds, y_at, ldy, kind, codes_at, scales_at, handle)
+    return NormOut(out, total_out, fp8)
 
 
 def quantize_fp8(x: torch.Tensor, scales: str = "mx", *, stream=None) -> FP8Rows:
     """bf16 or fp16 rows [rows, K] -> FP8Rows with one fp32 scale per row
     ("row", K a multiple of 8) or one power-of-two scale per 32 elements ("mx",
     a multiple of 32): nvfp4_quantize_rows_fp8.  K is at most 32768."""
-    ldx = _rows(x, "x")
-    T, K = x.shape
+    T, K, ldx, x_at = _rows(x, "x")
     _check_K(K)
     _check_scales(scales, K)
     handle, ctx = _on((x,), stream)
     with ctx:
         fp8 = _fp8_out(T, K, scales)
-        _lib.quantize_rows_fp8(_TYPES[x.dtype], x, ldx, T, K, _FP8[scales], fp8.codes, fp8.scales,
-                               handle)
+        _lib.quantize_rows_fp8(_TYPES[x.dtype], x_at, ldx, T, K, _FP8[scales],
+                               fp8.codes.data_ptr(), fp8.scales.data_ptr(), handle)
     return fp8
 
 
@@ -258,18 +262,17 @@ Operand = Union[torch.Tensor, FP8Rows]
 
 
 def _operand(v, name):
-    """(type, values, row stride, scales) of a linear operand, checked."""
-    scales = None
+    """(type, rows, K, row stride, address, values, scales, their address) of a
+    linear operand, checked."""
+    scales = scales_at = None
     if isinstance(v, torch.Tensor):
-        ld = _rows(v, name)
+        rows, K, ld, at = _rows(v, name)
         step, kind = 8, _TYPES[v.dtype]
-        K = v.shape[1]
     else:
         if not (isinstance(v, tuple) and len(v) == 2):
             raise ValueError(f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
         v, scales = v
-        ld = _rows(v, name, dtypes=_BYTES)
-        rows, K = v.shape
+        rows, K, ld, at = _rows(v, name, None, None, _BYTES)
         if not (isinstance(scales, torch.Tensor) and scales.is_contiguous()):
             raise ValueError(f"{name}'s scales must be a contiguous tensor")
         if scales.dtype == torch.float32:
@@ -279,9 +282,10 @@ def _operand(v, name):
             _need(scales.dtype == torch.uint8, "block scales must be uint8, row scales fp32")
         if scales.shape != shape:
             raise ValueError(f"{name}'s scales must be of shape {shape}")
+        scales_at = scales.data_ptr()
     if K < step or K % step:
         raise ValueError(f"{name} must have a multiple of {step} columns, not {K}")
-    return kind, v, ld, scales
+    return kind, rows, K, ld, at, v, scales, scales_at
 
 
 def _plain(t, name, shape, dtypes=_FLOATS):
@@ -320,15 +324,16 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     type by default, bf16 for FP8Rows), or FP8Rows with "mx" scales for
     out_dtype "mx" (N a multiple of 32).  `out` receives the result and may be
     the residual itself."""
-    kind, av, lda, a_sc = _operand(a, "a")
-    wkind, wv, ldw, w_sc = _operand(w, "w")
-    _need(kind == wkind, "a and w must be of one type, with one kind of scales")
-    M, K = av.shape
-    rows = wv.shape[0]
-    if wv.shape[1] != K:
+    kind, M, K, lda, a_at, av, a_sc, a_sc_at = _operand(a, "a")
+    wkind, rows, wK, ldw, w_at, wv, w_sc, w_sc_at = _operand(w, "w")
+    if kind != wkind:
+        raise ValueError("a and w must be of one type, with one kind of scales")
+    if wK != K:
         raise ValueError(f"w must have {K} columns, as a")
-    _need(gated is False or gated is True, "gated must be True or False")
-    _need(not gated or rows % 2 == 0, "a gated w has an even number of rows")
+    if not (gated is False or gated is True):
+        raise ValueError("gated must be True or False")
+    if gated and rows % 2:
+        raise ValueError("a gated w has an even number of rows")
     N = rows // 2 if gated else rows
     try:
         act_id = _ACTS[act]
@@ -367,12 +372,11 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
         else:
             res = _empty(M, N, out_dtype) if out is None else out
         p = _lib.Linear(
-            av.data_ptr(), None if a_sc is None else a_sc.data_ptr(), wv.data_ptr(),
-            None if w_sc is None else w_sc.data_ptr(), None if bias is None else bias.data_ptr(),
+            a_at, a_sc_at, w_at, w_sc_at, None if bias is None else bias.data_ptr(),
             None if residual is None else residual.data_ptr(), res.data_ptr(),
             None if out_scales is None else out_scales.data_ptr(), lda, ldw, ldr, ldo, M, N, K,
             kind, bias_type, res_type, out_type, act_id, gated)
         n = _workspace_bytes(M, N, K, kind, out_type, gated)
         ws = _empty_strided((n,), (1,), torch.uint8) if n else None
-        _lib.linear(p, ws, n, handle)
+        _lib.linear(p, None if ws is None else ws.data_ptr(), n, handle)
     return FP8Rows(res, out_scales) if mx else res
