@@ -11,7 +11,10 @@
 //
 // One group of kThreads threads owns a row and holds it in registers, 8
 // elements per 16-byte load, so every input is read once and every output
-// written once whatever combination of outputs is asked for.
+// written once whatever combination of outputs is asked for.  Bound by memory:
+// 8192 rows of 2816 with residual and all outputs (208 MB) take 32 to 35 us, what
+// a copy of that size takes (4.9 TB/s) and better where the last call's outputs
+// are still in the last-level cache; 16 rows take 4 us, a launch.
 #include "fp8_device.h"
 #include "internal.h"
 
@@ -192,9 +195,16 @@ hipError_t launch(const RowParams& p, hipStream_t stream) {
     }
     return hipSuccess;
   };
+  // One 16-byte vector per thread up to 2048 elements: the row's loads are all in
+  // flight at once and its reduction crosses the fewest wavefronts.  Measured as
+  // threads x vectors (norm with residual, all outputs, about 23 M elements / 16
+  // rows), us:       256: 32x1 15.0 / 3.2, 64x1 19.6 / 3.2;   704: 128x1 33.9 / 3.3,
+  // 64x2 35.6 / 3.9; 2048: 256x1 30.9 / 3.3, 128x2 31.3 / 3.9; 2816: 256x2 32.2 / 4.0,
+  // 512x1 32.9 / 3.6; 8192: 512x2 32.1 / 4.5, 256x4 33.4 / 5.3.
   if (nvec <= 16) return go(rows_kernel<kF16, kNorm, kFp8, 16, 1>, 16);
+  if (nvec <= 32) return go(rows_kernel<kF16, kNorm, kFp8, 32, 1>, 32);
   if (nvec <= 64) return go(rows_kernel<kF16, kNorm, kFp8, 64, 1>, 64);
-  if (nvec <= 128) return go(rows_kernel<kF16, kNorm, kFp8, 64, 2>, 64);
+  if (nvec <= 128) return go(rows_kernel<kF16, kNorm, kFp8, 128, 1>, 128);
   if (nvec <= 256) return go(rows_kernel<kF16, kNorm, kFp8, 256, 1>, 256);
   if (nvec <= 512) return go(rows_kernel<kF16, kNorm, kFp8, 256, 2>, 256);
   if (nvec <= 1024) return go(rows_kernel<kF16, kNorm, kFp8, 512, 2>, 512);

@@ -60,7 +60,7 @@ def norm_case(T, K, dtype, residual, weight, offset, scales, want_y=True, seed=0
 
 
 # each thread-group width of the kernel, whole and ragged, and its edges
-WIDTHS = [8, 24, 128, 136, 504, 512, 520, 1024, 1032, 2048, 2056, 2816, 4096, 4104, 8192, 8200, 16384, 16392, 32768]
+WIDTHS = [8, 24, 128, 136, 256, 264, 504, 512, 520, 1024, 1032, 2048, 2056, 2816, 4096, 4104, 8192, 8200, 16384, 16392, 32768]
 
 
 @pytest.mark.parametrize("K", WIDTHS)
