@@ -342,10 +342,10 @@ struct Prepared {
   uint32_t scale;
   __device__ __forceinline__ void set(const Frag& v, const uint32_t* s) { f = v; scale = s[0]; }
 };
-template <int kByte>
-struct PreparedWide {
+struct WideOp {
   bf16x8_t v[4];
-  __device__ __forceinline__ void set(const Frag& f, const uint32_t* s) {
+  template <int kByte>
+  __device__ __forceinline__ void widen(const Frag& f, const uint32_t* s) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       // 2^(code - 127), code in [1, 254]
@@ -354,6 +354,10 @@ struct PreparedWide {
       v[2 * c + 1] = widen8(f.c[c].z, f.c[c].w, scale);
     }
   }
+};
+template <int kByte>
+struct PreparedWide : WideOp {
+  __device__ __forceinline__ void set(const Frag& f, const uint32_t* s) { widen<kByte>(f, s); }
 };
 template <int kByte>
 struct Prepared<kRow8Wide, kByte> : PreparedWide<kByte> {};
@@ -571,6 +575,10 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   static_assert(kFM == 2 || kFM % 4 == 0, "fragment slots");
   constexpr int kAhead = kFM == 8 && kKind >= kRow8 ? 1 : 2;   // 8-bit fragments: one group, for want of registers
   constexpr int kWords = kKind == kBlock8Wide ? 2 : 1;         // scale words of a lane and row
+  // copies issued under the first matrix instructions after the barrier rather than
+  // right behind it: 8192^3 with block scales on 128-row tiles 650 -> 603 us, but
+  // bf16 on them 999 -> 1030
+  constexpr bool kLate = kKind >= kRow8 || kFM == 8;
   Frag fa[4], fw[kFN];
   uint32_t va[kFM][2], vw[kFN][2];
 #pragma unroll
@@ -637,7 +645,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
     // are on their way then are those of the steps from ks + 2 on
     if (kStages > 2 && ks + kStages <= steps) step_barrier<(kStages - 2) * kLoads>();
     else step_barrier<0>();
-    if (ks + kStages < steps) fetch(ks + kStages);
+    if (!kLate && ks + kStages < steps) fetch(ks + kStages);
     Op pa[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) pa[i].set(fa[(kBase + kFM - kAhead + i) & 3], va[kFM - kAhead + i]);
@@ -655,6 +663,63 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
       for (int i = kFM - kAhead; i < kFM; ++i) issued(acc[j][i]);
       fw[j] = read_frag(nw, j * 16 + i16, g);
       hold();
+      if (kLate && j == 0 && ks + kStages < steps) fetch(ks + kStages);
+    }
+  };
+  // The wide kinds' step where a wavefront has four groups: the conversions of each
+  // fragment stand among the matrix instructions before its first use (w's for the
+  // next step as soon as the last instruction on the old one is issued), two groups
+  // at a time, fragment of w by fragment of w.
+  constexpr bool kWideStep = is_wide(kKind) && kFM == 4;
+  WideOp ww[kWideStep ? kFN : 1], wa[2];
+  auto mix = [](auto valu) {                                   // eight matrix instructions, `valu` others after each
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, decltype(valu)::value, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto pair = [&](int j, int i0, const WideOp* a2) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc[j][i0 + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[j].v[u], a2[i].v[u], acc[j][i0 + i], 0, 0, 0);
+  };
+  auto wide_step = [&](auto t, int ks) {
+    constexpr int T = decltype(t)::value, N = (T + 1) % 4;
+    const char* ta = smem + (ks & (kStages - 1)) * kStage + wm * kTM * kStep;
+    const char* na = smem + ((ks + 1) & (kStages - 1)) * kStage + wm * kTM * kStep;
+    const char* nw = smem + ((ks + 1) & (kStages - 1)) * kStage + (kBM + wn * kTN) * kStep;
+    WideOp wb[2];
+    fa[2] = read_frag(ta, 32 + i16, g);
+    fa[3] = read_frag(ta, 48 + i16, g);
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) {
+      if (j == 0) ww[kFN - 1].template widen<T>(fw[kFN - 1], vw[kFN - 1]);
+      if (j == 1) wb[0].template widen<T>(fa[2], va[2]);
+      if (j == 2) wb[1].template widen<T>(fa[3], va[3]);
+      pair(j, 0, wa);
+      mix(std::integral_constant<int, 2>{});
+    }
+    if constexpr (kScaled) {
+      if constexpr (T == 1) scale_next = load_scales(scale_row, 4 * (step0 + ks + 3), nblk);
+      if constexpr (T == 2)
+        if (threadIdx.x < kBM + kBN) *reinterpret_cast<u32x4*>(s_scale[1 - ((ks >> 2) & 1)][threadIdx.x]) = scale_words(scale_next);
+    }
+    step_barrier<0>();
+    if constexpr (kScaled && T == 3) read_scales(((ks >> 2) + 1) & 1);
+    fa[0] = read_frag(na, i16, g);
+    fa[1] = read_frag(na, 16 + i16, g);
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) {
+      if (j > 0) ww[j - 1].template widen<N>(fw[j - 1], vw[j - 1]);
+      if (j >= 2) wa[j - 2].template widen<N>(fa[j - 2], va[j - 2]);
+      pair(j, 2, wb);
+      fw[j] = read_frag(nw, j * 16 + i16, g);
+      mix(std::integral_constant<int, 3>{});
+      if (j == 0 && ks + kStages < steps) fetch(ks + kStages);
     }
   };
   for (int ks = 0; ks < kStages && ks < steps; ++ks) fetch(ks);
@@ -665,15 +730,26 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + (kBM + wn * kTN) * kStep, j * 16 + i16, g);
   fa[0] = read_frag(smem + wm * kTM * kStep, i16, g);
   if (kAhead == 2) fa[1] = read_frag(smem + wm * kTM * kStep, 16 + i16, g);
+  if constexpr (kWideStep) {
+    if constexpr (kScaled) read_scales(0);
+#pragma unroll
+    for (int j = 0; j < kFN - 1; ++j) ww[j].template widen<0>(fw[j], vw[j]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) wa[i].template widen<0>(fa[i], va[i]);
+  }
+  auto run_step = [&](auto t, int ks) {
+    if constexpr (kWideStep) wide_step(t, ks);
+    else step(t, ks);
+  };
   for (int ks = 0;;) {
-    step(std::integral_constant<int, 0>{}, ks);
+    run_step(std::integral_constant<int, 0>{}, ks);
     if (++ks == steps) break;
-    step(std::integral_constant<int, 1>{}, ks);
+    run_step(std::integral_constant<int, 1>{}, ks);
     if (++ks == steps) break;
     if constexpr (kScaled) {
-      step(std::integral_constant<int, 2>{}, ks);
+      run_step(std::integral_constant<int, 2>{}, ks);
       if (++ks == steps) break;
-      step(std::integral_constant<int, 3>{}, ks);
+      run_step(std::integral_constant<int, 3>{}, ks);
       if (++ks == steps) break;
     }
   }
@@ -925,8 +1001,8 @@ struct Plan {
 struct Rate { float step, rest; };
 
 Rate rate_of(int kind, int kernel) {
-  if (kernel == kTile256) return {kind == kBlock8 ? 2.0f : 1.7f, 11.0f};
-  if (kernel == kTile128) return {is_wide(kind) ? 1.5f : kind == kBlock8 ? 1.3f : 1.0f, 4.0f};
+  if (kernel == kTile256) return {kind == kBlock8 ? 1.8f : 1.7f, 11.0f};
+  if (kernel == kTile128) return {is_wide(kind) ? 1.5f : kind == kBlock8 ? 1.2f : 1.0f, 4.0f};
   return {is_wide(kind) ? 0.8f : 0.42f, 2.0f};
 }
 
