@@ -20,29 +20,22 @@
 // fp32's own error.  fp32 outputs of 8-bit operands therefore run on the bf16
 // instruction: an E4M3 value times a power of two is a bf16 number, the products
 // are exact and the sums are fp32 sums (the "wide" kinds, at half the rate).
-#include <algorithm>
 #include <type_traits>
 
 #include "fp8_device.h"
 #include "internal.h"
+#include "linear_map.h"
 
 namespace nvfp4 {
 namespace {
+
+using namespace linear_map;
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// Operand kinds: 16-bit types, E4M3 with row or block scales, and the wide forms
-// of the latter two.
-enum { kBf16 = 0, kF16 = 1, kRow8 = 2, kBlock8 = 3, kRow8Wide = 4, kBlock8Wide = 5 };
-constexpr bool is_row8(int kind) { return kind == kRow8 || kind == kRow8Wide; }
-constexpr bool is_block8(int kind) { return kind == kBlock8 || kind == kBlock8Wide; }
-constexpr bool is_wide(int kind) { return kind == kRow8Wide || kind == kBlock8Wide; }
-enum { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutBlock8 = 3 };
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4 };
-
-constexpr int kStep = 128;                                     // bytes of K per step
 
 struct LinParams {
   const char* a;
@@ -447,24 +440,6 @@ __device__ __forceinline__ void step_barrier() {
   lds_barrier();
 }
 
-// The g-th of `total` workgroups in an order that gives each of the 8 XCDs (which
-// receive workgroups in turn) a contiguous range.
-__device__ __forceinline__ int32_t xcd_order(int32_t g, int32_t total) {
-  const int32_t per = total / 8, rest = total % 8, xcd = g % 8;
-  return xcd * per + (xcd < rest ? xcd : rest) + g / 8;
-}
-
-// Tile number -> (tile row, tile column): bands of 8 tile rows, each walked down
-// its columns, so that neighbours share rows of a and of w in their L2.
-__device__ __forceinline__ void tile_at(const LinParams& p, int32_t t, int32_t& tm, int32_t& tn) {
-  constexpr int32_t kBand = 8;
-  const int32_t band = t / (kBand * p.tiles_n);
-  const int32_t rows = min(kBand, p.tiles_m - band * kBand);
-  const int32_t in = t - band * kBand * p.tiles_n;
-  tm = band * kBand + in % rows;
-  tn = in / rows;
-}
-
 // ---- tiled kernel -------------------------------------------------------------
 // A workgroup of kWM x kWN wavefronts owns kBM rows of a and kBN rows of w
 // (gated: kBN / 2 output columns, their gate rows, then their up rows).  Each K
@@ -492,23 +467,11 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   const int wm = wave / kWN, wn = wave % kWN;
 
   // this workgroup's tile and K steps: all of them, or a part's
-  const int32_t total = p.tiles_m * p.tiles_n;
-  const bool whole = (int32_t)blockIdx.x < p.whole;
-  int32_t tile_no, part = 0, tm, tn;
-  if (whole) {
-    tile_no = xcd_order(blockIdx.x, p.whole);
-  } else {
-    const int32_t left = total - p.whole;
-    const int32_t q = xcd_order(blockIdx.x - p.whole, left * p.parts);
-    part = q / left;
-    tile_no = p.whole + q % left;
-  }
-  tile_at(p, tile_no, tm, tn);
-  const int step0 = part * p.part_steps;
-  const int all_steps = (p.kbytes + kStep - 1) / kStep;
-  const int steps = whole ? all_steps : min(p.part_steps, all_steps - step0);
-  const int64_t m0 = (int64_t)tm * kBM;
-  const int32_t n0 = tn * kOutN;
+  const Work work = work_at((int32_t)blockIdx.x, p.tiles_m, p.tiles_n, p.whole, p.parts, p.part_steps, p.kbytes);
+  const bool whole = work.part < 0;
+  const int step0 = work.step0, steps = work.steps;
+  const int64_t m0 = (int64_t)work.tm * kBM;
+  const int32_t n0 = work.tn * kOutN;
 
   // source of each copy: lane -> (row of the operand's tile, chunk).  Rows past the
   // edge repeat the last row, their results are not stored.  The offset from the
@@ -518,7 +481,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   const int first = wave * kLoads * 8;                         // the wavefront's first row of the tile
   const bool is_a = first < kBM;
   int row0 = (is_a ? first : (first - kBM) % kOutN) + (lane >> 3);
-  const int last_row = is_a ? (int)min((int64_t)kBM, p.M - m0) - 1 : min(kOutN, p.N - n0) - 1;
+  const int last_row = is_a ? last_row_of(kBM, p.M, m0) : last_row_of(kOutN, p.N, n0);
   const uint32_t ld = (uint32_t)(is_a ? p.lda : p.ldw);
   const int64_t up = kGated && !is_a ? (first - kBM) / kOutN * (int64_t)p.N : 0;
   uint64_t base = reinterpret_cast<uint64_t>((is_a ? p.a + m0 * p.lda : p.w + (n0 + up) * p.ldw) + (int64_t)step0 * kStep);
@@ -531,8 +494,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
       asm volatile("" : "+v"(row0));                           // (formed here, not carried along)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const uint32_t off = (uint32_t)min(row0 + 8 * i, last_row) * ld + chunk * 16;
-        copy_lds16(base, off, to + i * 1024);
+        copy_lds16(base, copy_offset(row0 + 8 * i, last_row, ld, chunk), to + i * 1024);
       }
     } else {                                                   // past the end of the rows
 #pragma unroll
@@ -802,7 +764,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
         }
       }
       if (!whole) {
-        float* sum = p.partial + (((int64_t)(tile_no - p.whole) * p.parts + part) * kBM + (m - m0)) * kBN + c;
+        float* sum = p.partial + partial_at(work.tile - p.whole, work.part, p.parts, (int)(m - m0), c, kBM, kBN);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           *reinterpret_cast<f32x4*>(sum + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
@@ -833,7 +795,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
   const int32_t r = (int32_t)(id / per % bm);
   const int32_t left = (int32_t)(id / ((int64_t)per * bm));
   int32_t tm, tn;
-  tile_at(p, p.whole + left, tm, tn);
+  tile_at(p.tiles_m, p.tiles_n, p.whole + left, tm, tn);
   const int64_t m = (int64_t)tm * bm + r;
   const int32_t n = tn * out_n + c;
   const bool in = m < p.M && n < p.N;
@@ -843,7 +805,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
   Residual<8> res;
   res.load(p, mr, n);
   float v[8] = {}, u[8] = {};
-  const float* sum = p.partial + ((int64_t)left * p.parts * bm + r) * bn + c;
+  const float* sum = p.partial + partial_at(left, 0, p.parts, r, c, bm, bn);
   for (int32_t part = 0; part < p.parts; ++part, sum += (int64_t)bm * bn) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -985,79 +947,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams
   }
 }
 
-// ---- choice of kernel and split -----------------------------------------------------
-enum { kFew, kTile64, kTile128, kTile256 };
-
-struct Plan {
-  int kernel;
-  int32_t tile, tiles_m, tiles_n;
-  int32_t whole, parts, part_steps;
-  size_t bytes;                                                // workspace
-};
-
-// What a launch takes, by measured rates in us: `step` per K step of a round (all
-// workgroups that the 256 CUs hold at once), `rest` per round (first copies and
-// epilogue).
-struct Rate { float step, rest; };
-
-Rate rate_of(int kind, int kernel) {
-  if (kernel == kTile256) return {kind == kBlock8 ? 1.8f : 1.7f, 11.0f};
-  if (kernel == kTile128) return {is_wide(kind) ? 1.5f : kind == kBlock8 ? 1.2f : 1.0f, 4.0f};
-  return {is_wide(kind) ? 0.8f : 0.42f, 2.0f};
-}
-
-// Tiles that fill whole rounds are computed whole.  Those of the last, partly
-// filled round may be cut along K into parts that fill it, at the price of a
-// second launch that joins the parts and of their sums' way to memory and back
-// (about 4 TB/s).
-Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) {
-  if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0};
-  const int32_t steps = (kbytes + kStep - 1) / kStep;
-  Plan best = {};
-  float best_cost = 0;
-  for (int kernel = kTile64; kernel <= (is_wide(kind) ? kTile128 : kTile256); ++kernel) {
-    const int32_t tile = kernel == kTile64 ? 64 : kernel == kTile128 ? 128 : 256;
-    const int32_t out_n = gated ? tile / 2 : tile;
-    const int32_t slots = kernel == kTile256 ? 256 : 512;
-    const int32_t threads = kernel == kTile256 ? 512 : 256;
-    Plan q = {kernel, tile, (M - 1) / tile + 1, (N - 1) / out_n + 1, 0, 1, steps, 0};
-    // a launch holds at most 2^32 - 1 threads (the callers' limit on sizes leaves
-    // room for tiles of 128)
-    if ((int64_t)q.tiles_m * q.tiles_n > 0x7FFFFFFF / threads) continue;
-    const int32_t total = q.tiles_m * q.tiles_n;
-    const Rate r = rate_of(kind, kernel);
-    const int32_t left = total % slots;
-    const float rounds = (float)(total / slots) * (steps * r.step + r.rest);
-    for (int32_t parts = 1; parts <= (left ? std::min(slots / left, 16) : 1); ++parts) {
-      // parts of whole groups of four steps (block scales come in fours)
-      int32_t each = parts == 1 ? steps : ((steps + parts - 1) / parts + 3) / 4 * 4;
-      const int32_t have = (steps + each - 1) / each;
-      if (have != parts) continue;
-      float cost = rounds;
-      if (left) cost += each * r.step + r.rest;
-      if (parts > 1) cost += 3.0f + (float)left * parts * tile * tile * 8.0f / 4e6f;
-      if (best_cost == 0 || cost < best_cost) {
-        best_cost = cost;
-        best = q;
-        best.parts = parts;
-        best.part_steps = each;
-        best.whole = parts > 1 ? total - left : total;
-        best.bytes = parts > 1 ? (size_t)left * parts * tile * tile * 4 : 0;
-      }
-    }
-  }
-  return best;
-}
-
-// 8-bit operands: the exact instructions where fp32's accuracy shows in the output
-// (fp32 itself; block scales, which change by a factor of two at a border) and where
-// reading w is the bound anyway.
-int kind_of(int kind, int32_t M, int32_t out_type) {
-  if (kind != kRow8 && kind != kBlock8) return kind;
-  if (M > 16 && out_type != kOutF32 && out_type != kOutBlock8) return kind;
-  return kind == kRow8 ? kRow8Wide : kBlock8Wide;
-}
-
+// ---- launches ------------------------------------------------------------------------
 template <int kKind, int kTile, int kWM, int kWN, int kStages, bool kGated>
 hipError_t go_tile(const LinParams& p, hipStream_t stream) {
   const int32_t left = p.tiles_m * p.tiles_n - p.whole;
