@@ -16,10 +16,13 @@
 // The scaled instruction adds its products in groups of eight and cuts each to a
 // multiple of 2^-13 of the group's largest power of two (found by its results):
 // sums of random data are off by about 1.5e-5 of their norm whatever K.  That is
-// nothing beside the rounding of a 16-bit or 8-bit output, but a hundred times
-// fp32's own error.  fp32 outputs of 8-bit operands therefore run on the bf16
-// instruction: an E4M3 value times a power of two is a bf16 number, the products
-// are exact and the sums are fp32 sums (the "wide" kinds, at half the rate).
+// nothing beside the rounding of a 16-bit output, but a hundred times fp32's own
+// error, and it moves block scales of an output, which change by a factor of two
+// at a border.  fp32 and block-scaled outputs of 8-bit operands therefore run on
+// the bf16 instruction: an E4M3 value times a power of two is a bf16 number, the
+// products are exact and the sums are fp32 sums (the "wide" kinds, at half the
+// rate: 4096 x 4224 x 2816 gated takes 73 us with the scaled instruction, 100 with
+// exact products).
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -446,6 +449,24 @@ __device__ __forceinline__ void step_barrier() {
 // step's rows are copied straight into LDS (kStages buffers).  The epilogue passes
 // the sums through LDS, 32 rows of each wavefront at a time, so that every thread
 // finishes 8 consecutive outputs of a row and whole rows are stored.
+//
+// Tiles.  A step of a 256 x 256 tile reads 64 KiB and multiplies 256 x 256 x 128
+// bytes: its eight wavefronts of 128 x 64 read 384 LDS rows per 128 matrix
+// instructions of 16 cycles, so LDS is busy a quarter of the time and the matrix
+// units set the pace.  8192^3, on 256 and on 128 tiles: bf16 860 to 900 us (1.22 to
+// 1.28 PFLOP/s) and 1032, row scales 440 to 458 (2.4 to 2.5 PFLOP/s) and 572, block
+// scales 466 to 481 and 625.  In bf16 the matrix units are busy 63 % of the cycles
+// at about 2.0 GHz (power holds the clock there), LDS 24 % with 1 % conflicts, and
+// 787 MB are read for 268 MB of operands; with block scales the matrix units are busy
+// 56 %.  128 x 128 tiles (two workgroups per CU) take the exact 8-bit products,
+// which need the registers for converted operands (8192^3 in 830 us, 1.32 PFLOP/s, the
+// bf16 instruction's rate), and sizes whose 256 tiles would leave CUs idle.
+// 64 x 64 tiles with four buffers take middle sizes, where latency and not
+// rate counts: 512 x 2816 x 2112 bf16 in 17.4 us on them, 30 on 128 tiles; 1000 x
+// 1411 x 704 fp16 11.4 and 21.
+// The 32x32x16 instructions were 3 % slower (902 against 876 us), copies issued
+// between the last instructions of a step 10 % (128 tiles), and four wavefronts of
+// 128 x 128 need more accumulators than the compiler keeps in place.
 template <int kKind, int kBM, int kBN, int kWM, int kWN, int kStages, bool kGated>
 __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const LinParams p) {
   constexpr int kWaves = kWM * kWN;
@@ -786,7 +807,11 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
 
 // ---- joining the parts -----------------------------------------------------------
 // The sums of a tile's parts, added in order, through the same epilogue; a thread
-// finishes 8 consecutive outputs of a row.
+// finishes 8 consecutive outputs of a row.  Bound by a launch and the sums' way
+// back from memory: 4.4 us for 4 parts of 4096 x 128, 6.0 us for the gated last round
+// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 205 and 235 us
+// (32 of 544 tiles in 4 parts), 4096 x 4224 x 2816 exact 103 to 108 and 116, 4096 x 128 x
+// 2816 15.9 and 17.2.
 template <int kKind, bool kGated>
 __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
   const int32_t out_n = kGated ? bn / 2 : bn, per = out_n / 8;
@@ -832,7 +857,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
 // registers.  A workgroup owns kCols output columns (gated: their gate and up
 // rows); its wavefronts take groups of four K steps in turn (a row's block scales
 // of a group are 16 bytes), kBatch steps' loads in flight at once, and their
-// partial sums are added in wavefront order through LDS.
+// partial sums are added in wavefront order through LDS.  1 x 8192 x 8192 takes 28 us
+// in bf16 (134 MB, 4.8 TB/s, a copy's rate) and 13.7 with 8 bits and row scales (4.9
+// TB/s); 16 x 8192 x 8192 with block scales 19.9 (3.5 TB/s: scales and conversions of w
+// come on top).  Small products are bound by a launch and one round of loads: 5 x
+// 2816 x 2112 in 4.5 us, 16 x 128 x 2816 in 7.3, whose eight workgroups each read 180 kB.
 template <int kKind, int kCols, int kWaves, bool kGated>
 __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams p) {
   constexpr int kRows = kGated ? 2 * kCols : kCols;            // rows of w

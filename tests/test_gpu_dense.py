@@ -382,6 +382,26 @@ def test_linear_nan_and_inf_stay_in_their_rows(kind):
         OD.check_rounded(f64(got)[~bad.numpy()], ref[~bad.numpy()], err[~bad.numpy()], F32)
 
 
+@pytest.mark.parametrize("M", [5, 40, 300])
+@pytest.mark.parametrize("ca,cw", [(1, 127), (3, 240), (7, 247), (240, 3), (127, 127)])
+def test_linear_block_scale_range(M, ca, cw):
+    """Scale codes towards the ends of their range.  Elements (2^-3 to 7.5) times
+    scales are normal numbers or multiples of 2^-133; other rows' scales of a
+    make the products' scale 1."""
+    g = torch.Generator().manual_seed(M + ca)
+    rows = lambda n: (torch.randint(0x20, 0x50, (n, 256), generator=g) +
+                      128 * torch.randint(0, 2, (n, 256), generator=g)).to(torch.uint8)
+    a, w = rows(M), rows(64)
+    sa = torch.full((M, 8), 254 - cw, dtype=torch.uint8)
+    sa[::2] = ca
+    sw = torch.full((64, 8), cw, dtype=torch.uint8)
+    av, wv = (OD.dequantize(c.numpy(), s.numpy()) for c, s in ((a, sa), (w, sw)))
+    for out in (F32, BF16):
+        ref, err = OD.linear(av, wv, scaled=scaled("mx", out))
+        got = D().linear(D().FP8Rows(a.cuda(), sa.cuda()), D().FP8Rows(w.cuda(), sw.cuda()), out_dtype=out)
+        OD.check_rounded(f64(got), ref, err, out)
+
+
 def test_offsets_past_32_bits():
     """Rows beyond 2^31 elements and 2^32 bytes of an operand, the residual and the
     result: the last rows are those of a call on them alone."""
