@@ -809,8 +809,8 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
 // The sums of a tile's parts, added in order, through the same epilogue; a thread
 // finishes 8 consecutive outputs of a row.  Bound by a launch and the sums' way
 // back from memory: 4.4 us for 4 parts of 4096 x 128, 6.0 us for the gated last round
-// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 205 and 235 us
-// (32 of 544 tiles in 4 parts), 4096 x 4224 x 2816 exact 103 to 108 and 116, 4096 x 128 x
+// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 197 and 209 us
+// (64 of 2112 tiles in 4 parts), 4096 x 4224 x 2816 exact 103 to 108 and 116, 4096 x 128 x
 // 2816 15.9 and 17.2.
 template <int kKind, bool kGated>
 __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
