@@ -13,9 +13,14 @@ experts, in 8 bits end to end:
 
 All functions raise ValueError for tensors of the wrong dtype, shape, layout
 or device, queue their work on `stream` (torch's current stream of the
-tensors' device when None; an integer is a raw HIP stream handle) and return
-without waiting.  They allocate through torch, so they can be captured into a
-graph.  Forward only: no gradients are recorded.
+tensors' device when None; an integer is a raw HIP stream handle, 0 the default
+stream) and return without waiting.  A `stream` that is not the current one
+neither waits for the work that makes the inputs, nor does later work of the
+current stream wait for it: the caller orders them, and marks results that
+other streams use (torch.Tensor.record_stream), since they are allocated on it.
+All memory comes through torch, so calls can be captured into a graph.  Sizes
+past the library's limits (linear: rows longer than 8 MiB, a result of more than
+2^36 elements) raise NVFP4Error.  Forward only: no gradients are recorded.
 """
 from __future__ import annotations
 
@@ -152,8 +157,9 @@ def _on(tensors, stream):
     if stream is None:
         return _raw_stream(index), _HERE if _current_device() == index else torch.cuda.device(index)
     dev = tensors[0].device
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if isinstance(stream, int):                                # (ExternalStream takes 0 for a new stream)
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    _need(isinstance(stream, torch.cuda.Stream), "stream must be a torch stream or a raw handle")
     _need(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
     if stream != torch.cuda.current_stream(dev):
         for t in tensors:

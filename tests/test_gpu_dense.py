@@ -510,6 +510,22 @@ def test_stream_argument(raw):
     assert torch.equal(want[1], got[1]) and torch.equal(want[2].codes, got[2].codes)
 
 
+def test_stream_zero_and_refused_streams():
+    x = rand((33, 128), 82).cuda()
+    want = D().quantize_fp8(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):                               # not the current stream: the default one
+        handle, ctx = D()._on((x,), 0)
+        with ctx:
+            assert handle == 0 and torch.cuda.current_stream() == torch.cuda.default_stream()
+        got = D().quantize_fp8(x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    with pytest.raises(ValueError):
+        D().quantize_fp8(x, stream="default")
+
+
 @pytest.mark.parametrize("T,sizes", [(3, SMALL), (290, SMALL), (20, MODEL), (150, MODEL)])
 def test_graph_replays(T, sizes):
     args = chain_inputs(T, 90, **sizes)
