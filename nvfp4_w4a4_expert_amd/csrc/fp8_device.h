@@ -55,10 +55,27 @@ __device__ __forceinline__ uint32_t encode4_e4m3(const float* y, float inv) {
   return (uint32_t)w;
 }
 
-// fp32 -> 16-bit pairs, rounded to nearest even.
+// The same for values whose products with inv are finite and at most 448.
+__device__ __forceinline__ uint32_t encode4_scaled(const float* y, float inv) {
+  int w = 0;
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * inv, y[1] * inv, w, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * inv, y[3] * inv, w, true);
+  return (uint32_t)w;
+}
+
+// Maximum over aligned groups of four lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
+  v = a > v ? a : v;
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
+  return b > v ? b : v;
+}
+
+// fp32 -> 16-bit pairs, rounded to nearest even (bf16: one instruction a pair).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |

@@ -66,14 +66,6 @@ __device__ __forceinline__ T group_reduce(T v, T* s_part, F f) {
   return v;
 }
 
-// Maximum over aligned groups of four lanes.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
-  v = a > v ? a : v;
-  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
-  return b > v ? b : v;
-}
-
 // kThreads threads per row, kVec 16-byte vectors per thread (K <= 8 * kThreads
 // * kVec); groups of at most a wavefront share a workgroup of 256 threads.
 template <bool kF16, bool kNorm, int kFp8, int kThreads, int kVec>
