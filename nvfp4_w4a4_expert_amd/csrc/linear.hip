@@ -21,7 +21,7 @@
 // at a border.  fp32 and block-scaled outputs of 8-bit operands therefore run on
 // the bf16 instruction: an E4M3 value times a power of two is a bf16 number, the
 // products are exact and the sums are fp32 sums (the "wide" kinds, at half the
-// rate: 4096 x 4224 x 2816 gated takes 73 us with the scaled instruction, 100 with
+// rate: 4096 x 4224 x 2816 gated takes 67 us with the scaled instruction, 96 with
 // exact products).
 #include <type_traits>
 
@@ -486,17 +486,17 @@ __device__ __forceinline__ void step_barrier() {
 // Tiles.  A step of a 256 x 256 tile reads 64 KiB and multiplies 256 x 256 x 128
 // bytes: its eight wavefronts of 128 x 64 read 384 LDS rows per 128 matrix
 // instructions of 16 cycles, so LDS is busy a quarter of the time and the matrix
-// units set the pace.  8192^3, on 256 and on 128 tiles: bf16 860 to 900 us (1.22 to
-// 1.28 PFLOP/s) and 1032, row scales 440 to 458 (2.4 to 2.5 PFLOP/s) and 572, block
-// scales 466 to 481 and 625.  In bf16 the matrix units are busy 63 % of the cycles
+// units set the pace.  8192^3, on 256 and on 128 tiles: bf16 840 us (1.31
+// PFLOP/s) and 979, row scales 429 (2.56 PFLOP/s) and 534, block scales 451 to 460 and
+// 595 (some machines take 5 % more).  In bf16 the matrix units are busy 63 % of the cycles
 // at about 2.0 GHz (power holds the clock there), LDS 24 % with 1 % conflicts, and
 // 787 MB are read for 268 MB of operands; with block scales the matrix units are busy
 // 56 %.  128 x 128 tiles (two workgroups per CU) take the exact 8-bit products,
 // which need the registers for converted operands (8192^3 in 830 us, 1.32 PFLOP/s, the
 // bf16 instruction's rate), and sizes whose 256 tiles would leave CUs idle.
 // 64 x 64 tiles with four buffers take middle sizes, where latency and not
-// rate counts: 512 x 2816 x 2112 bf16 in 17.4 us on them, 30 on 128 tiles; 1000 x
-// 1411 x 704 fp16 11.4 and 21.
+// rate counts: 512 x 2816 x 2112 bf16 in 17.2 us on them, 30 on 128 tiles; 1000 x
+// 1411 x 704 fp16 10.7 and 18.
 // The 32x32x16 instructions were 3 % slower (902 against 876 us), copies issued
 // between the last instructions of a step 10 % (128 tiles), and four wavefronts of
 // 128 x 128 need more accumulators than the compiler keeps in place.
@@ -842,9 +842,9 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
 // The sums of a tile's parts, added in order, through the same epilogue; a thread
 // finishes 8 consecutive outputs of a row.  Bound by a launch and the sums' way
 // back from memory: 4.4 us for 4 parts of 4096 x 128, 6.0 us for the gated last round
-// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 197 and 209 us
-// (64 of 2112 tiles in 4 parts), 4096 x 4224 x 2816 exact 103 to 108 and 116, 4096 x 128 x
-// 2816 15.9 and 17.2.
+// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 183 and 191 us
+// (64 of 2112 tiles in 4 parts), 4096 x 4224 x 2816 exact 96 and 108, 4096 x 128 x 2816
+// 15.6 and 17.3.
 template <int kKind, bool kGated>
 __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
   const int32_t out_n = kGated ? bn / 2 : bn, per = out_n / 8;

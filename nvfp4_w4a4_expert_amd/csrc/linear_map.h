@@ -51,10 +51,10 @@ inline Rate rate_of(int kind, int kernel) {
 // filled round may be cut along K into parts that fill it, at the price of a
 // second launch that joins the parts and of their sums' way to memory and back
 // (about 4 TB/s).  The model's choices against the others, in us: 8192 x 4224 x 2816
-// bf16 gated 128 tiles, the last 64 in 4 parts, 197; uncut 209; 256 tiles, the last
-// 32 in 4 parts, 205, uncut 235.  4096 x 2816 x 2112 with block scales 256 tiles 42.8; 128 tiles 49.4, their last
-// round cut 54.2; 64 tiles 76.5.  4096 x 128 x 2816 bf16 64 tiles in 4 parts 15.9, uncut
-// 17.2; 128 tiles in 6 parts 19.1, uncut 34.0.
+// bf16 gated 128 tiles, the last 64 in 4 parts, 183; uncut 191; 256 tiles, the last
+// 32 in 4 parts, 183, uncut 213.  4096 x 2816 x 2112 with block scales 256 tiles 41.4; 128
+// tiles 47.5, their last round cut 52.6; 64 tiles 74.1.  4096 x 128 x 2816 bf16 64 tiles
+// in 4 parts 15.6, uncut 17.3; 128 tiles in 6 parts 19.0, uncut 33.5.
 inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) {
   if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0};
   const int32_t steps = (kbytes + kStep - 1) / kStep;
