@@ -402,6 +402,30 @@ def test_linear_block_scale_range(M, ca, cw):
         OD.check_rounded(f64(got), ref, err, out)
 
 
+@pytest.mark.parametrize("M,N,K,gated", [(1, 32, 64, False), (9, 96, 128, True), (70, 160, 256, False), (300, 256, 192, True),
+                                         (260, 2112, 1024, True), (4096, 128, 2816, False)])
+@pytest.mark.parametrize("kind", ["bf16", "row", "mx"])
+def test_linear_mx_is_fp32_result_quantized(M, N, K, gated, kind):
+    """The 8-bit result is the quantiser's form of the fp32 one, code for code (both
+    run the same products and epilogue), with infinities, NaN and zero blocks among
+    the results."""
+    a, _ = operand((M, K), 90 + M, kind, 1.0)
+    w, _ = operand((2 * N if gated else N, K), 91 + N, kind, K ** -0.5)
+    b = rand((2 * N if gated else N,), 92, F32)
+    b[3], b[9], b[N // 2] = float("inf"), float("-inf"), float("nan")
+    r = rand((M, N), 93, F32)
+    r[M // 2, ::5] *= 2.0 ** 60
+    r[M // 3, 1] = float("nan")
+    kw = dict(bias=b.cuda(), gated=gated, act="relu" if gated else None, residual=r.cuda())
+    want = D().linear(a, w, out_dtype=F32, **kw)
+    got = D().linear(a, w, out_dtype="mx", **kw)
+    rc, rs = OD.quantize_block(f32(want))
+    c, s = fp8_np(got)
+    assert np.array_equal(s, rs)
+    nan = (rc & 0x7F) == 0x7F
+    assert nan.any() and np.array_equal(nan, (c & 0x7F) == 0x7F) and np.array_equal(rc[~nan], c[~nan])
+
+
 def test_offsets_past_32_bits():
     """Rows beyond 2^31 elements and 2^32 bytes of an operand, the residual and the
     result: the last rows are those of a call on them alone."""
