@@ -52,7 +52,9 @@ class MoEDebug(ctypes.Structure):
     ]
 
 
-class Linear(ctypes.Structure):
+class LinearFields(ctypes.Structure):
+    """nvfp4_linear_t.  ctypes drops the upper bits of a size past 32 bits; Linear
+    below refuses it."""
     _fields_ = [
         ("a", _p), ("a_scales", _p), ("w", _p), ("w_scales", _p),
         ("bias", _p), ("residual", _p), ("out", _p), ("out_scales", _p),
@@ -62,6 +64,18 @@ class Linear(ctypes.Structure):
         ("act", _i32), ("gated", _i32),
     ]
 
+
+class Linear(LinearFields):
+    """nvfp4_linear_t with sizes that fit its 32 bits, else NVFP4Error."""
+
+    def __init__(self, *args, **fields):
+        super().__init__(*args, **fields)
+        for name, given in [*zip(_LINEAR_NAMES, args), *fields.items()]:
+            if name in ("M", "N", "K"):
+                _check_size(given, f"nvfp4_linear_t.{name}")
+
+
+_LINEAR_NAMES = tuple(name for name, _ in LinearFields._fields_)
 
 FP8_NONE = -1
 TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_FP8_ROW, TYPE_FP8_MX = range(5)
@@ -100,8 +114,8 @@ _SIGS = {
     "nvfp4_rmsnorm": (_i32, [_i32, _p, _i64, _p, _i64, _p, ctypes.c_float, ctypes.c_float, _i32,
                              _i32, _p, _i64, _p, _i64, _i32, _p, _p, _p]),
     "nvfp4_quantize_rows_fp8": (_i32, [_i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
-    "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(Linear), ctypes.POINTER(ctypes.c_size_t)]),
-    "nvfp4_linear": (_i32, [ctypes.POINTER(Linear), _p, ctypes.c_size_t, _p]),
+    "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(LinearFields), ctypes.POINTER(ctypes.c_size_t)]),
+    "nvfp4_linear": (_i32, [ctypes.POINTER(LinearFields), _p, ctypes.c_size_t, _p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -129,6 +143,12 @@ def abi_version() -> int:
 def _check(status: int, where: str) -> None:
     if status != OK:
         raise NVFP4Error(status, where)
+
+
+def _check_size(n: int, where: str) -> None:
+    """The C entry points take sizes in 32 bits; ctypes would cut a longer one."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise NVFP4Error(ERR_UNSUPPORTED, f"{where} = {n}")
 
 
 def _ptr(t) -> Optional[int]:
@@ -302,6 +322,8 @@ def moe_forward_noalloc(weights: MoEWeights, x, router_logits, num_tokens: int, 
 
 def rmsnorm(*args):
     """The arguments of nvfp4_rmsnorm, in order."""
+    _check_size(args[8], "nvfp4_rmsnorm: num_rows")
+    _check_size(args[9], "nvfp4_rmsnorm: K")
     status = _lib.nvfp4_rmsnorm(*args)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_rmsnorm")
@@ -309,19 +331,21 @@ def rmsnorm(*args):
 
 def quantize_rows_fp8(*args):
     """The arguments of nvfp4_quantize_rows_fp8, in order."""
+    _check_size(args[3], "nvfp4_quantize_rows_fp8: num_rows")
+    _check_size(args[4], "nvfp4_quantize_rows_fp8: K")
     status = _lib.nvfp4_quantize_rows_fp8(*args)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_quantize_rows_fp8")
 
 
-def linear_workspace_size(p: Linear) -> int:
+def linear_workspace_size(p: LinearFields) -> int:
     n = ctypes.c_size_t()
     _check(_lib.nvfp4_linear_workspace_size(ctypes.byref(p), ctypes.byref(n)),
            "nvfp4_linear_workspace_size")
     return n.value
 
 
-def linear(p: Linear, workspace, workspace_bytes: int, stream):
+def linear(p: LinearFields, workspace, workspace_bytes: int, stream):
     status = _lib.nvfp4_linear(ctypes.byref(p), workspace, workspace_bytes, stream)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_linear")

@@ -19,8 +19,9 @@ neither waits for the work that makes the inputs, nor does later work of the
 current stream wait for it: the caller orders them, and marks results that
 other streams use (torch.Tensor.record_stream), since they are allocated on it.
 All memory comes through torch, so calls can be captured into a graph.  Sizes
-past the library's limits (linear: rows longer than 8 MiB, a result of more than
-2^36 elements) raise NVFP4Error.  Forward only: no gradients are recorded.
+past the library's limits (2^31 rows or more; linear: rows longer than 8 MiB, a
+result of more than 2^36 elements) raise NVFP4Error.  Forward only: no gradients
+are recorded.
 """
 from __future__ import annotations
 
@@ -82,6 +83,9 @@ def _rows(t, name, K=None, rows=None, dtypes=_HALF):
         raise ValueError(f"{name} must be a {want} [{'rows' if rows is None else rows}, "
                          f"{'K' if K is None else K}] tensor")
     T, K = shape
+    if T > 0x7FFFFFFF or K > 0x7FFFFFFF:                       # (before outputs are allocated)
+        _lib._check_size(T, f"rows of {name}")
+        _lib._check_size(K, f"columns of {name}")
     per16 = 16 // t.element_size()
     ld, step = t.stride()
     if T <= 1:
@@ -370,6 +374,7 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
             ldo = _plain(out, "out", (M, N), (out_dtype,))
             _check_apart(out, "out", (av, wv, a_sc, w_sc, bias))
             _check_apart(out, "out", (residual,), True)
+    n = _workspace_bytes(M, N, K, kind, out_type, gated)      # NVFP4Error past the limits, before anything is allocated
     handle, ctx = _on((av, wv, a_sc, w_sc, bias, residual, out), stream)
     with ctx:
         out_scales = None
@@ -377,12 +382,11 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
             res, out_scales = _fp8_out(M, N, "mx")
         else:
             res = _empty(M, N, out_dtype) if out is None else out
-        p = _lib.Linear(
+        p = _lib.LinearFields(                               # (a's and w's sizes are checked)
             a_at, a_sc_at, w_at, w_sc_at, None if bias is None else bias.data_ptr(),
             None if residual is None else residual.data_ptr(), res.data_ptr(),
             None if out_scales is None else out_scales.data_ptr(), lda, ldw, ldr, ldo, M, N, K,
             kind, bias_type, res_type, out_type, act_id, gated)
-        n = _workspace_bytes(M, N, K, kind, out_type, gated)
         ws = _empty_strided((n,), (1,), torch.uint8) if n else None
         _lib.linear(p, None if ws is None else ws.data_ptr(), n, handle)
     return FP8Rows(res, out_scales) if mx else res

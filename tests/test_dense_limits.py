@@ -1,0 +1,74 @@
+"""Sizes, scales and empty results at the ends of the dense operators' ranges,
+without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from nvfp4_w4a4_expert_amd import _lib as L
+from nvfp4_w4a4_expert_amd import dense as D
+
+BF16, U8 = torch.bfloat16, torch.uint8
+PAST = 2 ** 32                                               # 0 in 32 bits
+
+
+def meta(rows, cols, dtype=BF16):
+    """A tensor of any size without memory."""
+    return torch.empty(rows, cols, dtype=dtype, device="meta")
+
+
+# ---- sizes that 32 bits do not hold ------------------------------------------------
+
+@pytest.mark.parametrize("rows", [2 ** 31, PAST, PAST + 5])
+def test_row_counts_past_32_bits_are_refused(rows):
+    x = meta(rows, 32)
+    w, q = meta(8, 32), (meta(8, 32, U8), torch.empty(8, 1, dtype=U8, device="meta"))
+    many = (meta(rows, 32, U8), torch.empty(rows, 1, dtype=U8, device="meta"))
+    for call in (lambda: D.rms_norm(x), lambda: D.rms_norm(x, residual=x, scales="mx"), lambda: D.quantize_fp8(x),
+                 lambda: D.quantize_fp8(x, "row"), lambda: D.linear(x, w), lambda: D.linear(w, x),
+                 lambda: D.linear(w, x, gated=True), lambda: D.linear(many, q), lambda: D.linear(q, many)):
+        with pytest.raises(L.NVFP4Error, match=str(rows)) as e:
+            call()
+        assert e.value.status == L.ERR_UNSUPPORTED
+
+
+def test_columns_past_32_bits_are_refused():
+    with pytest.raises(L.NVFP4Error, match=str(PAST + 64)):
+        D.linear(meta(2, PAST + 64), meta(3, PAST + 64))
+
+
+def test_results_past_the_limit_are_refused_before_they_are_allocated():
+    for a, w, kw in ((meta(1 << 30, 64), meta(1 << 20, 64), {}), (meta(1 << 30, 64), meta(1 << 20, 64), dict(gated=True)),
+                     (meta(4, 64), meta((1 << 24) + 32, 64), dict(out_dtype="mx")), (meta(2, (1 << 22) + 8), meta(3, (1 << 22) + 8), {})):
+        with pytest.raises(L.NVFP4Error) as e:
+            D.linear(a, w, **kw)
+        assert e.value.status == L.ERR_UNSUPPORTED
+
+
+def test_last_row_count_of_32_bits_is_taken():
+    with pytest.raises(ValueError, match="on a GPU"):
+        D.quantize_fp8(meta(2 ** 31 - 1, 32))
+
+
+@pytest.mark.parametrize("n", [2 ** 31, PAST, PAST + 5, -2 ** 31 - 1])
+def test_binding_refuses_sizes_that_it_would_cut(n):
+    norm = [L.TYPE_BF16, None, 64, None, 0, None, 0.0, 1e-6, 0, 64, None, 0, None, 64, L.FP8_NONE, None, None, None]
+    quant = [L.TYPE_BF16, None, 64, 0, 64, L.TYPE_FP8_MX, None, None, None]
+    L.rmsnorm(*norm)                                         # no rows: nothing to do
+    L.quantize_rows_fp8(*quant)
+    for f, args, places in ((L.rmsnorm, norm, (8, 9)), (L.quantize_rows_fp8, quant, (3, 4))):
+        for at in places:
+            bad = list(args)
+            bad[at] = n
+            with pytest.raises(L.NVFP4Error) as e:
+                f(*bad)
+            assert e.value.status == L.ERR_UNSUPPORTED
+    for kw in (dict(M=n), dict(N=n), dict(K=n)):
+        with pytest.raises(L.NVFP4Error) as e:
+            L.Linear(**kw)
+        assert e.value.status == L.ERR_UNSUPPORTED
+    with pytest.raises(L.NVFP4Error):
+        L.Linear(*[None] * 8, *[64] * 4, n, 32, 64)
+    p = L.Linear(M=2 ** 31 - 1, N=0, K=64, type=L.TYPE_BF16)
+    assert p.M == 2 ** 31 - 1 and isinstance(p, L.LinearFields) and L.linear_workspace_size(p) == 0
+    assert ctypes.sizeof(L.Linear) == ctypes.sizeof(L.LinearFields)
