@@ -53,7 +53,7 @@ class FP8Rows(NamedTuple):
         if self.scales.dtype == torch.float32:
             return v * self.scales[:, None]
         s = self.scales.view(torch.float8_e8m0fnu).float()
-        return (v.view(v.shape[0], -1, 32) * s[..., None]).view(v.shape)
+        return (v.view(*s.shape, 32) * s[..., None]).view(v.shape)
 
 
 class NormOut(NamedTuple):

@@ -72,3 +72,22 @@ def test_binding_refuses_sizes_that_it_would_cut(n):
     p = L.Linear(M=2 ** 31 - 1, N=0, K=64, type=L.TYPE_BF16)
     assert p.M == 2 ** 31 - 1 and isinstance(p, L.LinearFields) and L.linear_workspace_size(p) == 0
     assert ctypes.sizeof(L.Linear) == ctypes.sizeof(L.LinearFields)
+
+
+# ---- results without rows ------------------------------------------------------------
+
+def test_dequantize_of_no_rows():
+    for scales in (torch.zeros(0, 2, dtype=U8), torch.zeros(0)):
+        v = D.FP8Rows(torch.zeros(0, 64, dtype=U8), scales).dequantize()
+        assert v.shape == (0, 64) and v.dtype == torch.float32
+
+
+def test_dequantize_of_strided_codes_and_end_scales():
+    codes = torch.arange(3 * 160, dtype=torch.int32).remainder(127).to(U8).view(3, 160)[:, 32:96]
+    scales = torch.tensor([[0, 127], [254, 1], [255, 130]], dtype=U8)
+    v = D.FP8Rows(codes, scales).dequantize()
+    want = codes.contiguous().view(torch.float8_e4m3fn).double().view(3, 2, 32) * (2.0 ** (scales.double() - 127))[..., None]
+    want = want.view(3, 64)
+    ok = torch.ones(3, 64, dtype=torch.bool)
+    ok[2, :32] = False                                       # scale code 255 is NaN
+    assert v[~ok].isnan().all() and torch.equal(v[ok], want[ok].float())

@@ -81,3 +81,13 @@ def test_small_and_zero_sums_under_huge_row_scales(M):
     b = torch.ones(N)
     got = D().linear(a, w, bias=b.cuda(), out_dtype=F32)
     assert (got[:, 1::2] == 1).all()
+
+
+# ---- results without rows --------------------------------------------------------------
+
+def test_empty_results_dequantize():
+    x = torch.zeros(0, 64, dtype=BF16, device="cuda")
+    w = torch.zeros(32, 64, dtype=BF16, device="cuda")
+    for r, cols in ((D().rms_norm(x, scales="mx").fp8, 64), (D().rms_norm(x, scales="row").fp8, 64), (D().quantize_fp8(x, "mx"), 64),
+                    (D().quantize_fp8(x, "row"), 64), (D().linear(x, w, out_dtype="mx"), 32)):
+        assert r.dequantize().shape == (0, cols)
