@@ -91,3 +91,54 @@ def test_empty_results_dequantize():
     for r, cols in ((D().rms_norm(x, scales="mx").fp8, 64), (D().rms_norm(x, scales="row").fp8, 64), (D().quantize_fp8(x, "mx"), 64),
                     (D().quantize_fp8(x, "row"), 64), (D().linear(x, w, out_dtype="mx"), 32)):
         assert r.dequantize().shape == (0, cols)
+
+
+# ---- sums of the scaled instruction ----------------------------------------------------
+
+def cancelling(rows, K, rng, sign):
+    """In each group of eight two large elements, whose products with the other
+    operand's cancel exactly (sign -1 on one side), among small ones."""
+    c = (rng.integers(0x20, 0x40, (rows, K)) | 128 * rng.integers(0, 2, (rows, K))).astype(np.uint8)
+    big = (rng.integers(0x60, 0x7F, (rows, K // 8)) | 128 * rng.integers(0, 2, (rows, K // 8))).astype(np.uint8)
+    c[:, 1::8] = big
+    c[:, 5::8] = big ^ (0x80 if sign < 0 else 0)
+    return c
+
+
+DATA = {"random": lambda n, K, rng, s: OD.e4m3_encode(np.clip(rng.standard_normal((n, K)) * 100, -448, 448)),
+        "positive": lambda n, K, rng, s: OD.e4m3_encode(np.clip(np.abs(rng.standard_normal((n, K))) * 100, 0, 448)),
+        "every code": lambda n, K, rng, s: (rng.integers(0, 0x7F, (n, K)) | 128 * rng.integers(0, 2, (n, K))).astype(np.uint8),
+        "cancelling": cancelling}
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 33, 160), (65, 96, 512), (300, 130, 1056), (1500, 2816, 544), (4096, 2816, 2112)])
+@pytest.mark.parametrize("kind", ["row", "mx"])
+@pytest.mark.parametrize("data", list(DATA))
+def test_scaled_sums_follow_the_cut(M, N, K, kind, data):
+    """16-bit results of 8-bit operands are the cut sums (OD.cut_sums) to fp32 accuracy
+    and one rounding, for sums of one sign and for sums that cancel as well; on some
+    rows and columns of every tile."""
+    from nvfp4_w4a4_expert_amd import _lib as L
+    for out, t in ((BF16, L.TYPE_BF16), (F16, L.TYPE_FP16)):
+        p = L.Linear(M=M, N=N, K=K, type=L.TYPE_FP8_ROW if kind == "row" else L.TYPE_FP8_MX, out_type=t)
+        assert L.linear_workspace_size(p) == 0                 # one run over K, as in cut_sums
+    rng = np.random.default_rng(M + N)
+    ca, cw = DATA[data](M, K, rng, 1), DATA[data](N, K, rng, -1)
+    i = np.unique(np.r_[0:3, rng.integers(0, M, 40), M - 3:M])
+    j = np.unique(np.r_[0:3, rng.integers(0, N, 50), N - 3:N])
+    if kind == "row":
+        sa, sw = (rng.uniform(0.5, 2, n).astype(np.float32) * np.float32(2.0 ** -12 / K) ** 0.5 for n in (M, N))
+        sa, sw = sa.astype(np.float32), sw.astype(np.float32)
+        s, err = OD.cut_sums(OD.e4m3_decode(ca[i]), OD.e4m3_decode(cw[j]))
+        both = sa[i].astype(np.float64)[:, None] * sw[j].astype(np.float64)[None]
+        s, err = s * both, err * both + 2 * OD.U * np.abs(s * both)
+    else:
+        # (down to about 1 / sqrt(K) of E4M3's size, so that fp16 holds the results)
+        sa, sw = (rng.integers(119, 122, (n, K // 32)).astype(np.uint8) for n in (M, N))
+        s, err = OD.cut_sums(OD.dequantize(ca[i], sa[i]), OD.dequantize(cw[j], sw[j]))
+    a = D().FP8Rows(torch.from_numpy(ca).cuda(), torch.from_numpy(sa).cuda())
+    w = D().FP8Rows(torch.from_numpy(cw).cuda(), torch.from_numpy(sw).cuda())
+    assert np.abs(s).max() < 6e4
+    for out in (BF16, F16):
+        got = f64(D().linear(a, w, out_dtype=out))[np.ix_(i, j)]
+        OD.check_rounded(got, s, err, out, f"{kind} {data} {out}")
