@@ -82,7 +82,7 @@ __device__ __forceinline__ float half_exp(float x) {
 
 // erfc(x) by the Chebyshev fit t * exp(-x^2 + P(t)), t = 1 / (1 + |x| / 2), of
 // Press et al., Numerical Recipes (the routine of fractional error below
-// 1.2e-7 everywhere), so gelu keeps its relative accuracy where erfc is tiny.
+// 1.2e-7 everywhere), so gelu does not cancel where erfc is tiny.
 __device__ __forceinline__ float erfc_fit(float x) {
   const float z = fabsf(x), t = __builtin_amdgcn_rcpf(1.0f + 0.5f * z);
   float q = 0.17087277f;
@@ -103,10 +103,13 @@ __device__ __forceinline__ float erfc_fit(float x) {
 // The activations over a run of values: silu and gelu's tanh form as v *
 // sigmoid(z) (z = 2u for the latter: 1 + tanh u would cancel for negative u),
 // gelu's erf form as v * erfc(-v / sqrt 2) / 2.  With the exponential and the
-// reciprocal instructions (a step each) a value is off by about 12 half steps of
-// fp32, in about 20 instructions where expf() and a division took 45 (4096 x 4224 x 2816
-// exact, gated, 103 -> 100 us; 8192 x 4224 x 2816 bf16 190 -> 187): the epilogue is bound
-// by the instructions it issues.
+// reciprocal instructions (a step each) a value of silu is off by at most 12 + z / 4
+// half steps of fp32, of gelu's tanh form by 12 + 3 z and of its erf form by 16 + 4 z,
+// where z is the exponent for v < 0 (|v|, |2u|, v^2 / 2; 0 for v >= 0): the
+// roundings of z itself are not carried, and count only where the result is exp(-z)
+// of v.  It takes about 20 instructions where expf() and a division took 45 (4096 x
+// 4224 x 2816 exact, gated, 103 -> 100 us; 8192 x 4224 x 2816 bf16 190 -> 187): the
+// epilogue is bound by the instructions it issues.
 template <int kLen>
 __device__ __forceinline__ void activate_run(float* v, int32_t act) {
   if (act == kActNone) return;

@@ -132,13 +132,33 @@ def activate(v, act):
         return np.maximum(v, 0) if act == "relu" else v
 
 
+def activation_error(v, act):
+    """Bound on an activation's evaluation in fp32, in half steps u of its value.  With
+    z the exponent (exp(-z) is what a small result is made of), exp(z / 2) from a base-2
+    exponential and a reciprocal of one step each, and their products, give 12 u.  Then
+    u per unit of z times what z is off by, in u: silu takes v itself (1/4 for the
+    constant's rounding), gelu_tanh rounds two constants, a square, a sum and a
+    product (3), gelu a constant, its product with v and the sum that holds v^2 / 2
+    (4), and 4 u more for erfc's fit (fractional 1.2e-7) and halving.  A host model
+    of the code, its exponential and reciprocal off by a step, stays below these
+    (z = 87: 29, 233 and 283)."""
+    a = np.abs(v)
+    neg = v < 0
+    if act == "silu":
+        return 12 + np.where(neg, np.minimum(a, 180), 0) / 4
+    if act == "gelu_tanh":
+        return 12 + 3 * np.where(neg, np.minimum(2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3), 180), 0)
+    if act == "gelu":
+        return 16 + 4 * np.where(neg, np.minimum(a * a / 2, 180), 0)
+    return np.zeros_like(a)
+
+
 def linear(a, w, bias=None, act=None, gated=False, residual=None, scaled=False):
     """(out, fp32 error bound), all float64.  Sums: one rounding per step of a
     32-deep matrix instruction and a budget of 64 for the instruction's own sum
     and the scales' products, relative to sum |a w|; |act'| <= 1.2 for every
-    activation (gelu's slope peaks at 1.13); its evaluation is off by at most
-    (16 + 4 |v|) u of its value plus 16 u |v| for erfc's fit (fractional 1.2e-7
-    and the rounded argument of exp); product, residual: one rounding each.
+    activation (gelu's slope peaks at 1.13); its evaluation is off as
+    activation_error says; product, residual: one rounding each.
 
     scaled: 8-bit operands on the scaled matrix instruction, which cuts each
     product to a multiple of 2^-13 of the largest power of two among its group
@@ -159,8 +179,7 @@ def linear(a, w, bias=None, act=None, gated=False, residual=None, scaled=False):
     g, ge = v[:, :N], e[:, :N]
     out = activate(g, act)
     err = 1.2 * ge
-    if act not in (None, "none", "relu"):
-        err = err + (16 + 4 * np.abs(g)) * U * np.abs(out) + 16 * U * np.abs(g)
+    err = err + activation_error(g, act) * U * np.abs(out) + 2.0 ** -145
     if gated:
         u, ue = v[:, N:], e[:, N:]
         err = np.abs(u) * err + np.abs(out) * ue + err * ue

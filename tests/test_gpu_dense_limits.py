@@ -142,3 +142,22 @@ def test_scaled_sums_follow_the_cut(M, N, K, kind, data):
     for out in (BF16, F16):
         got = f64(D().linear(a, w, out_dtype=out))[np.ix_(i, j)]
         OD.check_rounded(got, s, err, out, f"{kind} {data} {out}")
+
+
+# ---- activations -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 20])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activation_error(act, M):
+    """act(v) for fp32 v (the bias of a product of zeros) within the half steps that
+    its exponent allows (OD.activation_error), also where the result is tiny."""
+    rng = np.random.default_rng(3)
+    v = np.concatenate([rng.uniform(-1, 1, 3000) * s for s in (1e-3, 1, 4, 16)] +
+                       [rng.uniform(-i - 1, -i, 1000) for i in range(15)] + [rng.uniform(-90, 90, 4000)]).astype(np.float32)
+    a = torch.zeros(M, 8, dtype=BF16, device="cuda")
+    w = torch.zeros(v.size, 8, dtype=BF16, device="cuda")
+    got = f64(D().linear(a, w, bias=torch.from_numpy(v).cuda(), act=act, out_dtype=F32))
+    x = v.astype(np.float64)
+    ref = OD.activate(x, act)
+    off = np.abs(got - ref) - OD.activation_error(x, act) * OD.U * np.abs(ref) - 2.0 ** -145
+    assert np.all(off <= 0), (act, v[off.max(0).argmax()])
