@@ -531,8 +531,9 @@ NVFP4_API nvfp4_status_t nvfp4_moe_forward_mx(const nvfp4_moe_weights_t* w, cons
  *       scale = fl32(amax / 448), code = E4M3(fl32(y * inv)),
  *       inv = min(fl32(1 / scale), FLT_MAX), or 0 when scale is 0;
  *   NVFP4_TYPE_FP8_MX   one UE8M0 scale per 32 consecutive elements, uint8
- *       [rows, K/32], value 2^(scale - 127): the smallest power of two P with
- *       amax <= 448 P, clamped to [2^-126, 2^127]; code = E4M3(y / P).
+ *       [rows, K/32], value 2^(scale - 127), 255 NaN.  Made here: the smallest
+ *       power of two P with amax <= 448 P, clamped to [2^-126, 2^127]; code =
+ *       E4M3(y / P).
  * E4M3() rounds to nearest, ties to even, and saturates at 448.  amax is over
  * finite elements; an infinite or NaN element becomes the E4M3 NaN.
  */
@@ -627,7 +628,7 @@ typedef enum {
  *                  rows [0, N) gate, [N, 2N) up); 16-byte aligned, row strides
  *                  a multiple of 16 bytes, >= K.
  *   a_scales, w_scales  of the 8-bit types: device float [rows] or uint8
- *                  [rows, K/32] (codes 1 to 254); ignored otherwise.
+ *                  [rows, K/32] (255 is NaN); ignored otherwise.
  *   K              >= 1; K % 8 == 0 (16-bit types), % 16 (FP8_ROW), % 32 (FP8_MX).
  *   bias           device [N] ([2N] when gated) of bias_type, or NULL.
  *   residual       device [M, ldr] of residual_type, or NULL.

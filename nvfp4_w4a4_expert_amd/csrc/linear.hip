@@ -412,7 +412,8 @@ struct WideOp {
   __device__ __forceinline__ void widen(const Frag& f, const uint32_t* s) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      // 2^(code - 127), code in [1, 254]
+      // 2^(code - 127): the conversion reads the exponent alone, so code 0 is 2^-127 and
+      // 255 NaN, as for the scaled instruction
       const float scale = __uint_as_float(((s[c] >> (8 * kByte)) & 0xFFu) << 23);
       v[2 * c] = widen8(f.c[c].x, f.c[c].y, scale);
       v[2 * c + 1] = widen8(f.c[c].z, f.c[c].w, scale);

@@ -161,3 +161,34 @@ def test_activation_error(act, M):
     ref = OD.activate(x, act)
     off = np.abs(got - ref) - OD.activation_error(x, act) * OD.U * np.abs(ref) - 2.0 ** -145
     assert np.all(off <= 0), (act, v[off.max(0).argmax()])
+
+
+# ---- block scales' first and last codes --------------------------------------------------
+
+@pytest.mark.parametrize("M", [5, 40, 300])
+@pytest.mark.parametrize("cw", [134, 247])
+def test_block_scale_codes_0_and_255(M, cw):
+    """Code 0 is 2^-127 and 255 is NaN, in the exact and in the scaled products, for
+    blocks with elements (multiples of 2^-133 here) and for blocks of zeros."""
+    rng = np.random.default_rng(M)
+    N, K = 70, 256
+    ca, cw_ = row_codes(M, K, rng), row_codes(N, K, rng)
+    ca[1::3, 32:64] = 0                                        # blocks of zeros under code 0
+    sa = np.where(rng.random((M, K // 32)) < 0.5, 254 - cw, 0).astype(np.uint8)
+    sa[:, 1] = 0
+    sa[0] = 0
+    sw = np.full((N, K // 32), cw, np.uint8)
+    sw[3, 5] = 0
+    a_nan, w_nan = sa.copy(), sw.copy()
+    a_nan[2, 7], w_nan[9, 0] = 255, 255
+    for out in (F32, BF16):
+        ops = lambda s, t: (D().FP8Rows(torch.from_numpy(ca).cuda(), torch.from_numpy(s).cuda()),
+                            D().FP8Rows(torch.from_numpy(cw_).cuda(), torch.from_numpy(t).cuda()))
+        ref, err = OD.linear(OD.dequantize(ca, sa), OD.dequantize(cw_, sw), scaled=out != F32)
+        assert np.abs(ref[0]).max() > 0                        # a row of code 0 alone has values
+        got = f64(D().linear(*ops(sa, sw), out_dtype=out))
+        OD.check_rounded(got, ref, err + 2.0 ** -149, out)
+        bad = f64(D().linear(*ops(a_nan, w_nan), out_dtype=out))
+        want = np.zeros((M, N), bool)
+        want[2], want[:, 9] = True, True
+        assert np.array_equal(np.isnan(bad), want) and np.array_equal(bad[~want], got[~want])
