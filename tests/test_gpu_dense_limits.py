@@ -192,3 +192,97 @@ def test_block_scale_codes_0_and_255(M, cw):
         want = np.zeros((M, N), bool)
         want[2], want[:, 9] = True, True
         assert np.array_equal(np.isnan(bad), want) and np.array_equal(bad[~want], got[~want])
+
+
+# ---- launches in parts, threads, other allocators ----------------------------------------
+
+def test_rows_past_one_launch():
+    """2^21 rows fill one launch of the row operators: the next launch's first and last
+    rows are as exact as the first one's."""
+    T, K = 2 ** 21 + 37, 32
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(1)).to(BF16)
+    at = np.r_[0:40, 2 ** 21 - 40:T]
+    xs = x[at].float().numpy()
+    dx = x.cuda()
+    for scales, oracle in (("row", OD.quantize_row), ("mx", OD.quantize_block)):
+        q = D().quantize_fp8(dx, scales)
+        c, s = oracle(xs)
+        assert np.array_equal(q.codes.cpu().numpy()[at], c) and np.array_equal(q.scales.cpu().numpy()[at], s)
+        r = D().rms_norm(dx, residual=dx, scales=scales)
+        total = (2 * x.float()).to(BF16)
+        assert torch.equal(r.total.cpu(), total)
+        y, err = OD.rms_norm(f64(total[at]), None, 1e-6, 0.0)
+        OD.check_rounded(f64(r.y)[at], y, err, BF16, scales)
+        OD.check_fp8(r.fp8.codes.cpu().numpy()[at], r.fp8.scales.cpu().numpy()[at], y, err, scales)
+
+
+def layer_calls(seed):
+    g = torch.Generator().manual_seed(seed)
+    x, h = (torch.randn(40, 256, generator=g).to(BF16).cuda() for _ in range(2))
+    w = torch.randn(320, 256, generator=g).to(BF16).cuda()
+    d = torch.randn(256, 160, generator=g).to(BF16).cuda()
+    r = torch.randn(24, 256, generator=g).to(BF16).cuda()
+
+    def run(mod):
+        n = mod.rms_norm(x, residual=h, scales="mx")
+        a = mod.linear(n.fp8, mod.quantize_fp8(w), act="gelu_tanh", gated=True, out_dtype="mx")
+        out = mod.linear(a, mod.quantize_fp8(d), residual=n.total)
+        return [n.y, n.total, *n.fp8, mod.linear(n.y, r, out_dtype=F32), *a, out, mod.quantize_fp8(x, "row").codes]
+    return run
+
+
+def test_threads_calling_at_once():
+    """Threads with a stream each, calling at the same time, each get the results of
+    their own inputs."""
+    import threading
+    D()
+    calls = [layer_calls(s) for s in range(4)]
+    want = [run(D()) for run in calls]
+    torch.cuda.synchronize()
+    got, go = [None] * 4, threading.Barrier(4)
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                go.wait(30)
+                res = [calls[i](D()) for _ in range(15)]
+            stream.synchronize()
+            got[i] = res
+        except Exception as e:
+            got[i] = e
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    for g, w in zip(got, want):
+        assert isinstance(g, list), g
+        for res in g:
+            assert all(torch.equal(p, q) for p, q in zip(res, w))
+
+
+def test_without_torchs_own_shortcuts(monkeypatch):
+    """Where torch lacks the private functions that small calls go through, the public
+    ones give the same, on another stream as well."""
+    import importlib.util
+    assert D()._raw_stream is torch._C._cuda_getCurrentRawStream         # the shortcuts are taken here
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.delattr(torch._C, "_cuda_getDevice")
+    monkeypatch.delattr(torch._C._dynamo.guards, "_empty_strided_cuda")
+    spec = importlib.util.spec_from_file_location("nvfp4_w4a4_expert_amd.dense_public", D().__file__)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    monkeypatch.undo()
+    assert mod._raw_stream is not D()._raw_stream and mod._empty_strided is not D()._empty_strided
+    assert mod._raw_stream(0) == torch.cuda.current_stream().cuda_stream and mod._current_device() == 0
+    run = layer_calls(9)
+    want = run(D())
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(run(mod), want))
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        assert mod._raw_stream(0) == stream.cuda_stream
+        got = run(mod)
+    stream.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
