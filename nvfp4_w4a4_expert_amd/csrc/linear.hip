@@ -567,16 +567,13 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
   // edge repeat the last row, their results are not stored.  The offset from the
   // tile's first row is formed at each copy (three instructions): kept for all
   // copies, it would cost the registers that the fragments need.
-  const int chunk = (lane & 7) ^ (lane >> 3);                  // (row & 7) == lane >> 3
-  const int first = wave * kLoads * 8;                         // the wavefront's first row of the tile
-  const bool is_a = first < kBM;
-  int row0 = (is_a ? first : (first - kBM) % kOutN) + (lane >> 3);
-  const int last_row = is_a ? last_row_of(kBM, p.M, m0) : last_row_of(kOutN, p.N, n0);
-  const uint32_t ld = (uint32_t)(is_a ? p.lda : p.ldw);
-  const int64_t up = kGated && !is_a ? (first - kBM) / kOutN * (int64_t)p.N : 0;
-  uint64_t base = reinterpret_cast<uint64_t>((is_a ? p.a + m0 * p.lda : p.w + (n0 + up) * p.ldw) + (int64_t)step0 * kStep);
-  // bytes of the last step
-  const int tail = min(p.kbytes - (step0 + steps - 1) * kStep, kStep);
+  const Copies from = copies_at(wave, lane, kLoads, kBM, kOutN);
+  const int chunk = from.chunk;
+  int row0 = from.row0;
+  const int last_row = from.of_a ? last_row_of(kBM, p.M, m0) : last_row_of(kOutN, p.N, n0);
+  const uint32_t ld = (uint32_t)(from.of_a ? p.lda : p.ldw);
+  uint64_t base = reinterpret_cast<uint64_t>((from.of_a ? p.a : p.w) + copy_base(from, m0, n0, p.N, p.lda, p.ldw, step0));
+  const int tail = last_bytes(p.kbytes, step0, steps);
   auto fetch = [&](int ks) {
     char* dst = smem + (ks & (kStages - 1)) * kStage + wave * kLoads * 1024;
     if (chunk * 16 < (ks == steps - 1 ? tail : kStep)) {

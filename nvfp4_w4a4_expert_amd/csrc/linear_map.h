@@ -153,6 +153,38 @@ NVFP4_LINEAR_HD int32_t last_row_of(int32_t rows, int32_t have, int64_t from) {
   return (int32_t)(have - from < rows ? have - from : rows) - 1;
 }
 
+// What a lane of a wavefront copies of each step: from `first` on, 8 * loads rows of
+// the operands' tiles (bm rows of a, then out_n rows of w, gated a further out_n),
+// all of one operand; the lane's rows are row0, row0 + 8, ... of that part (gate and
+// up rows counted apart), its 16 bytes those of `chunk`.
+struct Copies {
+  bool of_a, of_up;
+  int32_t row0, chunk;
+};
+
+NVFP4_LINEAR_HD Copies copies_at(int32_t wave, int32_t lane, int32_t loads, int32_t bm, int32_t out_n) {
+  const int32_t first = wave * loads * 8;
+  Copies c;
+  c.of_a = first < bm;
+  c.of_up = first >= bm + out_n;
+  c.row0 = (c.of_a ? first : (first - bm) % out_n) + (lane >> 3);
+  c.chunk = (lane & 7) ^ (lane >> 3);                          // (row & 7) == lane >> 3
+  return c;
+}
+
+// Offset in its operand of the part's first row, at the first step: tile rows from m0
+// (a) or n0 (w, whose up rows follow its N gate rows) on; strides in bytes.
+NVFP4_LINEAR_HD int64_t copy_base(const Copies& c, int64_t m0, int32_t n0, int32_t N, int64_t lda, int64_t ldw,
+                                  int32_t step0) {
+  return (c.of_a ? m0 * lda : (n0 + (c.of_up ? (int64_t)N : 0)) * ldw) + (int64_t)step0 * kStep;
+}
+
+// Bytes of a row in the last of `steps` steps from step0 on.
+NVFP4_LINEAR_HD int32_t last_bytes(int32_t kbytes, int32_t step0, int32_t steps) {
+  const int32_t left = kbytes - (step0 + steps - 1) * kStep;
+  return left < kStep ? left : kStep;
+}
+
 // Offset of a lane's 16 bytes from its operand's tile at a step: row of the tile
 // (at most the last one) and chunk of the step.
 NVFP4_LINEAR_HD uint32_t copy_offset(int32_t row, int32_t last_row, uint32_t ld, int32_t chunk) {
