@@ -26,8 +26,8 @@
 // at a border.  fp32 and block-scaled outputs of 8-bit operands therefore run on
 // the bf16 instruction: an E4M3 value times a power of two is a bf16 number, the
 // products are exact and the sums are fp32 sums (the "wide" kinds, at half the
-// rate: 4096 x 4224 x 2816 gated takes 67 us with the scaled instruction, 96 with
-// exact products).
+// rate: 4096 x 4224 x 2816 gated with block scales takes 69 us with the scaled
+// instruction, 98 with exact products).
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -522,17 +522,17 @@ __device__ __forceinline__ void step_barrier() {
 // Tiles.  A step of a 256 x 256 tile reads 64 KiB and multiplies 256 x 256 x 128
 // bytes: its eight wavefronts of 128 x 64 read 384 LDS rows per 128 matrix
 // instructions of 16 cycles, so LDS is busy a quarter of the time and the matrix
-// units set the pace.  8192^3, on 256 and on 128 tiles: bf16 840 us (1.31
-// PFLOP/s) and 979, row scales 429 (2.56 PFLOP/s) and 534, block scales 451 to 460 and
-// 595 (some machines take 5 % more).  In bf16 the matrix units are busy 63 % of the cycles
-// at about 2.0 GHz (power holds the clock there), LDS 24 % with 1 % conflicts, and
-// 787 MB are read for 268 MB of operands; with block scales the matrix units are busy
-// 56 %.  128 x 128 tiles (two workgroups per CU) take the exact 8-bit products,
-// which need the registers for converted operands (8192^3 in 830 us, 1.32 PFLOP/s, the
-// bf16 instruction's rate), and sizes whose 256 tiles would leave CUs idle.
-// 64 x 64 tiles with four buffers take middle sizes, where latency and not
-// rate counts: 512 x 2816 x 2112 bf16 in 17.2 us on them, 30 on 128 tiles; 1000 x
-// 1411 x 704 fp16 10.7 and 18.
+// units set the pace.  8192^3, on 256 and on 128 tiles: bf16 833 to 906 us (1.32 to
+// 1.21 PFLOP/s, as power holds the clock, 1.5 to 2.0 GHz) and 994 to 1047, row scales 443
+// to 500 (2.48 to 2.20 PFLOP/s) and 511 to 536, block scales 446 to 465 and 557 to 581.
+// The matrix units are busy 64 % of the cycles in bf16, 61 % with row and 58 % with block
+// scales, LDS 25 to 27 % with up to 2 % conflicts; 1.6 GB are read for 268 MB of bf16
+// operands.  128 x 128 tiles (two workgroups per CU) take the exact 8-bit products,
+// which need the registers for converted operands (8192^3 in 821 to 859 us with row
+// scales, the bf16 instruction's rate, 914 to 942 with block scales), and sizes whose
+// 256 tiles would leave CUs idle.  64 x 64 tiles with four buffers take middle sizes,
+// where latency and not rate counts: 512 x 2816 x 2112 bf16 in 16.1 to 17.6 us on them,
+// 24 on 128 tiles; 1000 x 1411 x 704 fp16 10.6 and 16.8.
 // The 32x32x16 instructions were 3 % slower (902 against 876 us), copies issued
 // between the last instructions of a step 10 % (128 tiles), and four wavefronts of
 // 128 x 128 need more accumulators than the compiler keeps in place.
@@ -875,9 +875,10 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Li
 // The sums of a tile's parts, added in order, through the same epilogue; a thread
 // finishes 8 consecutive outputs of a row.  Bound by a launch and the sums' way
 // back from memory: 4.4 us for 4 parts of 4096 x 128, 6.0 us for the gated last round
-// of 8192 x 2112.  With and without the cut: 8192 x 4224 x 2816 bf16 gated 183 and 191 us
-// (64 of 2112 tiles in 4 parts), 4096 x 4224 x 2816 exact 96 and 108, 4096 x 128 x 2816
-// 15.6 and 17.3.
+// of 8192 x 2112.  With and without the cut (inputs in the last-level cache / from
+// memory): 8192 x 4224 x 2816 bf16 gated 191 and 197 us / 223 and 244 (64 of 2112 tiles
+// in 4 parts), 4096 x 4224 x 2816 exact 102 and 110 / 110 and 119, 4096 x 128 x 2816 15.6
+// and 17.1 / 18.2 and 18.4.
 template <int kKind, bool kGated>
 __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
   const int32_t out_n = kGated ? bn / 2 : bn, per = out_n / 8;
@@ -923,11 +924,12 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
 // registers.  A workgroup owns kCols output columns (gated: their gate and up
 // rows); its wavefronts take groups of four K steps in turn (a row's block scales
 // of a group are 16 bytes), kBatch steps' loads in flight at once, and their
-// partial sums are added in wavefront order through LDS.  1 x 8192 x 8192 takes 28 us
-// in bf16 (134 MB, 4.8 TB/s, a copy's rate) and 13.7 with 8 bits and row scales (4.9
-// TB/s); 16 x 8192 x 8192 with block scales 19.9 (3.5 TB/s: scales and conversions of w
-// come on top).  Small products are bound by a launch and one round of loads: 5 x
-// 2816 x 2112 in 4.5 us, 16 x 128 x 2816 in 7.3, whose eight workgroups each read 180 kB.
+// partial sums are added in wavefront order through LDS.  With w from memory 1 x 8192 x 8192
+// takes 29.0 us in bf16 (134 MB, 4.6 TB/s) and 16.7 with 8 bits and row scales (4.0 TB/s),
+// 16 x 8192 x 8192 with block scales 25.3 (2.7 TB/s: scales and conversions of w come on
+// top); with w in the last-level cache 25.0, 14.3 and 19.9.  Small products are bound by
+// a launch and one round of loads: 5 x 2816 x 2112 in 4.7 us, 16 x 128 x 2816 in 7.2,
+// whose eight workgroups each read 180 kB.
 template <int kKind, int kCols, int kWaves, bool kGated>
 __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams p) {
   constexpr int kRows = kGated ? 2 * kCols : kCols;            // rows of w

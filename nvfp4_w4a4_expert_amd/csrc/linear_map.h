@@ -50,11 +50,15 @@ inline Rate rate_of(int kind, int kernel) {
 // Tiles that fill whole rounds are computed whole.  Those of the last, partly
 // filled round may be cut along K into parts that fill it, at the price of a
 // second launch that joins the parts and of their sums' way to memory and back
-// (about 4 TB/s).  The model's choices against the others, in us: 8192 x 4224 x 2816
-// bf16 gated 128 tiles, the last 64 in 4 parts, 183; uncut 191; 256 tiles, the last
-// 32 in 4 parts, 183, uncut 213.  4096 x 2816 x 2112 with block scales 256 tiles 41.4; 128
-// tiles 47.5, their last round cut 52.6; 64 tiles 74.1.  4096 x 128 x 2816 bf16 64 tiles
-// in 4 parts 15.6, uncut 17.3; 128 tiles in 6 parts 19.0, uncut 33.5.
+// (about 4 TB/s).  The model's choices against the others, in us, as replays of a
+// graph on one set of inputs (in the last-level cache) / on sets of over 800 MB in
+// turn (from memory).  8192 x 4224 x 2816 bf16 gated: 128 tiles, the last 64 in 4 parts,
+// 191 / 223 (chosen; between calls from Python, outputs in turn, 202); uncut 197 / 244;
+// 256 tiles, the last 32 in 4 parts, 193 / 207; uncut 220 / 230: the rates tell the two
+// tiles apart by less than the inputs' place does.  4096 x 2816 x 2112 with block scales:
+// 256 tiles 40.4 / 46.9 (chosen), 128 tiles 44.8 / 58.5, 64 tiles 69.9 / 86.4.  4096 x 128
+// x 2816 bf16: 64 tiles in 4 parts 15.6 / 18.2 (chosen), uncut 17.1 / 18.4; 128 tiles in
+// 6 parts 18.9 / 22.0, uncut 27.2 / 51.
 inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) {
   if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0};
   const int32_t steps = (kbytes + kStep - 1) / kStep;

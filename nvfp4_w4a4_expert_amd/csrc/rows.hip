@@ -12,9 +12,10 @@
 // One group of kThreads threads owns a row and holds it in registers, 8
 // elements per 16-byte load, so every input is read once and every output
 // written once whatever combination of outputs is asked for.  Bound by memory:
-// 8192 rows of 2816 with residual and all outputs (208 MB) take 32 to 35 us, what
-// a copy of that size takes (4.9 TB/s) and better where the last call's outputs
-// are still in the last-level cache; 16 rows take 4 us, a launch.
+// 8192 rows of 2816 with residual and all outputs (208 MB) take 37 us on ten sets of
+// tensors in turn (5.6 TB/s; a copy of that size, in turn as well, 39 to 42), and 28 to
+// 35 on one set, most of which the last-level cache still holds from the call before;
+// 16 rows take 4 us, a launch.
 #include "fp8_device.h"
 #include "internal.h"
 
@@ -190,7 +191,7 @@ hipError_t launch(const RowParams& p, hipStream_t stream) {
   // One 16-byte vector per thread up to 2048 elements: the row's loads are all in
   // flight at once and its reduction crosses the fewest wavefronts.  Measured as
   // threads x vectors (norm with residual, all outputs, about 23 M elements / 16
-  // rows), us:       256: 32x1 15.0 / 3.2, 64x1 19.6 / 3.2;   704: 128x1 33.9 / 3.3,
+  // rows, on one set of tensors, partly in the last-level cache), us:       256: 32x1 15.0 / 3.2, 64x1 19.6 / 3.2;   704: 128x1 33.9 / 3.3,
   // 64x2 35.6 / 3.9; 2048: 256x1 30.9 / 3.3, 128x2 31.3 / 3.9; 2816: 256x2 32.2 / 4.0,
   // 512x1 32.9 / 3.6; 8192: 512x2 32.1 / 4.5, 256x4 33.4 / 5.3.
   if (nvec <= 16) return go(rows_kernel<kF16, kNorm, kFp8, 16, 1>, 16);
