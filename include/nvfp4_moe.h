@@ -553,11 +553,10 @@ typedef enum {
  *         residual);
  *     y = s * (1 / sqrt(mean(s^2) + eps)) * (weight_offset + weight), in fp32.
  * y_out receives y rounded once, codes / scales the 8-bit form of the fp32 y.
- * The mean is an fp32 sum: rows whose sum of squares passes 3.4e38 give 0 (bf16
- * elements beyond about 1e19 only), and with eps = 0 a row whose sum is 0 (all
- * elements below about 1e-22) gives infinities, and NaN for its zeros.  A row with
- * a NaN gives NaN throughout, one with an infinity NaN there and 0 elsewhere, in
- * every output.
+ * The mean is an fp32 sum; rows whose squares leave fp32's range are scaled by a
+ * power of two first, so every finite row has the formula's values (with eps = 0 a
+ * row of zeros is 0 / 0: NaN).  A row with a NaN gives NaN throughout, one with an
+ * infinity NaN there and 0 elsewhere, in every output.
  *
  *   type            NVFP4_TYPE_BF16 or NVFP4_TYPE_FP16: x, residual, weight,
  *                   sum_out and y_out.

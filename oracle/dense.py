@@ -78,11 +78,12 @@ def dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     return e4m3_decode(codes) * scale_values(scales, codes.shape[1])
 
 
-def check_fp8(codes, scales, y, err, label=""):
+def check_fp8(codes, scales, y, err, label="", lost=0.0):
     """codes / scales hold float64 values y known to the kernel up to `err`: the
     scale belongs to an amax within err, and each code is the E4M3 number
     nearest to a value within err of y / scale.  E4M3's half step is 2^-4 of the
-    value, at least 2^-10 (subnormals are multiples of 2^-9)."""
+    value, at least 2^-10 (subnormals are multiples of 2^-9).  lost: what the codes
+    alone may be off by besides."""
     K = y.shape[1]
     err = np.broadcast_to(err, y.shape)
     if scales.dtype == np.uint8:
@@ -100,7 +101,7 @@ def check_fp8(codes, scales, y, err, label=""):
     mag = np.abs(y) + err
     tol = np.maximum(mag * 2.0 ** -4, sv * 2.0 ** -10) * (1 + 2.0 ** -20) + err + s_err * mag
     # a row or block without a nonzero element has scale 0 (row) or codes 0
-    off = np.abs(got - y) - tol
+    off = np.abs(got - y) - tol - lost
     assert np.all(off <= 0), f"{label}: code off by {off.max():.3g} over its bound"
 
 

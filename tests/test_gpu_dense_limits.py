@@ -286,3 +286,43 @@ def test_without_torchs_own_shortcuts(monkeypatch):
         got = run(mod)
     stream.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+# ---- rows whose squares leave fp32's range -----------------------------------------------
+
+@pytest.mark.parametrize("K", [24, 128, 256, 512, 1024, 2048, 4096, 8192, 16384, 32768])
+def test_norm_of_rows_past_the_range_of_squares(K):
+    """Finite rows of any size have the formula's values, side by side with ordinary
+    rows, infinities and NaN (rows of one wavefront among them)."""
+    rng = np.random.default_rng(K)
+    sizes = [1.0, 1e30, 2.0 ** -66, 1e-30, 2.5e18, 3e19, 2.0 ** -110, 1.0, 1e25, 2.0 ** -128, 5e37, 1e-19, 1.0]
+    x = torch.from_numpy(np.clip(rng.standard_normal((len(sizes), K)), -3, 3) * np.array(sizes)[:, None]).to(BF16)
+    extra = torch.zeros(6, K, dtype=BF16)
+    extra[0] = torch.finfo(BF16).max
+    extra[1, 5], extra[1, 7] = 1e30, 1.0                       # one huge element
+    extra[2] = 2.0 ** -133                                     # the smallest bf16 number
+    extra[3, 9] = float("inf")
+    extra[3, 2] = 1e30
+    extra[4] = 1e30
+    extra[4, 11] = float("nan")
+    extra[5, 3] = -2.0 ** -133
+    x = torch.cat([x, extra])
+    bad = np.array([len(sizes) + 3, len(sizes) + 4])
+    good = np.setdiff1d(np.arange(x.shape[0]), bad)
+    w = torch.from_numpy(rng.standard_normal(K)).to(BF16)
+    for eps in (0.0, 2.0 ** -90, 1e-6, 1e38):
+        for scales in ("row", "mx") if K % 32 == 0 else ("row",):
+            n = D().rms_norm(x.cuda(), w.cuda(), eps=eps, weight_offset=1.0, scales=scales)
+            y, err = OD.rms_norm(f64(x)[good], f64(w), float(np.float32(eps)), 1.0)
+            err = err + 2.0 ** -140
+            OD.check_rounded(f64(n.y)[good], y, err, BF16, f"{K} {eps}")
+            c, s = n.fp8.codes.cpu().numpy(), n.fp8.scales.cpu().numpy()
+            # Row form: code = E4M3(y * min(1 / scale, FLT_MAX)).  Where scale = amax / 448 is below
+            # 1 / FLT_MAX the second factor is less than 1 / scale, so code * scale lies between 0
+            # and y up to the code's own rounding: off by up to |y| by definition.
+            low = np.abs(y).max(1, keepdims=True) < 448 * 2.0 ** -128 * (1 + 2.0 ** -10)
+            lost = np.where(low, np.abs(y), 0) if scales == "row" else 0
+            OD.check_fp8(c[good], s[good], y, err, f"{K} {eps} {scales}", lost)
+            z = f64(n.y)[bad]
+            assert np.isnan(z[1]).all() and np.isnan(z[0, 9]) and not np.delete(z[0], 9).any()
+            assert np.all((c[bad[1]] & 0x7F) == 0x7F) and not (np.delete(c[bad[0]], 9) & 0x7F).any()
