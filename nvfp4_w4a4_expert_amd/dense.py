@@ -66,6 +66,7 @@ class NormOut(NamedTuple):
 _HALF = (torch.bfloat16, torch.float16)
 _BYTES = (torch.uint8,)
 _FLOATS = tuple(_TYPES)
+_STRIDED = torch.strided
 
 
 def _need(ok, msg):
@@ -77,7 +78,7 @@ def _rows(t, name, K=None, rows=None, dtypes=_HALF):
     """(rows, K, row stride, address) of a 2-D tensor whose rows are contiguous
     and start on 16-byte boundaries (the stride of one row, which is arbitrary,
     as if it were followed by another)."""
-    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes else ()
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.layout is _STRIDED else ()
     if len(shape) != 2 or (K is not None and shape[1] != K) or (rows is not None and shape[0] != rows):
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be a {want} [{'rows' if rows is None else rows}, "
@@ -217,7 +218,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     elif not want_y and scales is None:
         raise ValueError("nothing is asked for: want_y, scales or a residual")
     if weight is not None:
-        if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and
+        if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and weight.layout is _STRIDED and
                 weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0):
             raise ValueError(f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
         w_at = weight.data_ptr()
@@ -283,7 +284,7 @@ def _operand(v, name):
             raise ValueError(f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
         v, scales = v
         rows, K, ld, at = _rows(v, name, None, None, _BYTES)
-        if not (isinstance(scales, torch.Tensor) and scales.is_contiguous()):
+        if not (isinstance(scales, torch.Tensor) and scales.layout is _STRIDED and scales.is_contiguous()):
             raise ValueError(f"{name}'s scales must be a contiguous tensor")
         if scales.dtype == torch.float32:
             step, kind, shape = 16, _lib.TYPE_FP8_ROW, (rows,)
@@ -300,7 +301,7 @@ def _operand(v, name):
 
 def _plain(t, name, shape, dtypes=_FLOATS):
     """The row stride of a tensor of `shape` with contiguous rows, aligned to its type."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape:
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.layout is _STRIDED:
         st = t.stride()
         if len(shape) == 1:
             if st[0] == 1 or shape[0] <= 1:

@@ -115,3 +115,20 @@ def test_oracle_cut_sums():
     one = np.zeros((1, 8))
     one[0, 0], one[0, 7] = 256.0, 1.125
     assert OD.cut_sums(one, np.abs(one))[0] == 65536 and OD.cut_sums(np.roll(one, 4, 1), -np.abs(np.roll(one, 4, 1)))[0] == -65536
+
+
+# ---- tensors without strides ---------------------------------------------------------
+
+def test_sparse_tensors_are_refused():
+    """As every tensor of a wrong layout: with ValueError."""
+    x, w = torch.zeros(4, 64, dtype=BF16), torch.zeros(64, dtype=BF16)
+    q = (torch.zeros(4, 64, dtype=U8), torch.zeros(4))
+    m = (torch.zeros(4, 64, dtype=U8), torch.zeros(4, 2, dtype=U8))
+    sp = lambda t: t.to_sparse()
+    for call in (lambda: D.rms_norm(sp(x)), lambda: D.rms_norm(x, sp(w)), lambda: D.rms_norm(x, residual=sp(x)),
+                 lambda: D.rms_norm(x, out=sp(x)), lambda: D.quantize_fp8(sp(x)), lambda: D.linear(sp(x), x),
+                 lambda: D.linear(x, sp(x)), lambda: D.linear(x, x, bias=sp(torch.zeros(4))),
+                 lambda: D.linear(x, x, residual=sp(torch.zeros(4, 4))), lambda: D.linear(x, x, out=sp(torch.zeros(4, 4))),
+                 lambda: D.linear((sp(q[0]), q[1]), q), lambda: D.linear(q, (q[0], sp(q[1]))), lambda: D.linear((m[0], sp(m[1])), m)):
+        with pytest.raises(ValueError, match="^(?!.*on a GPU)"):
+            call()
