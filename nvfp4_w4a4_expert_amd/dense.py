@@ -66,7 +66,6 @@ class NormOut(NamedTuple):
 _HALF = (torch.bfloat16, torch.float16)
 _BYTES = (torch.uint8,)
 _FLOATS = tuple(_TYPES)
-_STRIDED = torch.strided
 
 
 def _need(ok, msg):
@@ -78,7 +77,7 @@ def _rows(t, name, K=None, rows=None, dtypes=_HALF):
     """(rows, K, row stride, address) of a 2-D tensor whose rows are contiguous
     and start on 16-byte boundaries (the stride of one row, which is arbitrary,
     as if it were followed by another)."""
-    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.layout is _STRIDED else ()
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype in dtypes else ()
     if len(shape) != 2 or (K is not None and shape[1] != K) or (rows is not None and shape[0] != rows):
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be a {want} [{'rows' if rows is None else rows}, "
@@ -91,10 +90,10 @@ def _rows(t, name, K=None, rows=None, dtypes=_HALF):
     ld, step = t.stride()
     if T <= 1:
         ld = -(-K // per16) * per16
-    at = t.data_ptr()
-    if (ld < K or ld % per16 or (step != 1 and K != 1) or at % 16) and T and K:
+    # (the strides first: those of a sparse tensor are 0, and it has no address)
+    if (ld < K or ld % per16 or (step != 1 and K != 1) or t.data_ptr() % 16) and T and K:
         raise ValueError(f"{name}'s rows must be contiguous and start on 16-byte boundaries")
-    return T, K, ld, at
+    return T, K, ld, t.data_ptr()
 
 
 def _span(t):
@@ -218,7 +217,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     elif not want_y and scales is None:
         raise ValueError("nothing is asked for: want_y, scales or a residual")
     if weight is not None:
-        if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and weight.layout is _STRIDED and
+        if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and
                 weight.shape == (K,) and weight.is_contiguous() and weight.data_ptr() % 16 == 0):
             raise ValueError(f"weight must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
         w_at = weight.data_ptr()
@@ -284,7 +283,7 @@ def _operand(v, name):
             raise ValueError(f"{name} must be a bf16 or fp16 tensor or an FP8Rows")
         v, scales = v
         rows, K, ld, at = _rows(v, name, None, None, _BYTES)
-        if not (isinstance(scales, torch.Tensor) and scales.layout is _STRIDED and scales.is_contiguous()):
+        if not (isinstance(scales, torch.Tensor) and scales.is_contiguous()):
             raise ValueError(f"{name}'s scales must be a contiguous tensor")
         if scales.dtype == torch.float32:
             step, kind, shape = 16, _lib.TYPE_FP8_ROW, (rows,)
@@ -301,7 +300,7 @@ def _operand(v, name):
 
 def _plain(t, name, shape, dtypes=_FLOATS):
     """The row stride of a tensor of `shape` with contiguous rows, aligned to its type."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.layout is _STRIDED:
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape:
         st = t.stride()
         if len(shape) == 1:
             if st[0] == 1 or shape[0] <= 1:
