@@ -596,6 +596,60 @@ NVFP4_API nvfp4_status_t nvfp4_quantize_rows_fp8(int32_t type, const void* x, in
                                                  uint8_t* codes, void* scales,
                                                  nvfp4_stream_t stream);
 
+/* Functions of a gate tensor (nvfp4_block_norm). */
+typedef enum {
+  NVFP4_GATE_PLAIN = 0,
+  NVFP4_GATE_SIGMOID = 1,   /* 1 / (1 + exp(-v)) */
+  NVFP4_GATE_TANH = 2
+} nvfp4_gate_t;
+
+/*
+ * nvfp4_block_norm — the end of one block and the start of the next in one pass over
+ * the rows: the block's last norm, its gate, the residual stream's addition, the next
+ * block's first norm and its 8-bit form:
+ *     b = x * (1 / sqrt(mean(x^2) + eps)) * (weight_offset + post_weight), in fp32
+ *         (x itself when post is 0);
+ *     t = rnd(residual_scale * residual + gate_scale * gate_act(gate) * b), rounded to
+ *         the tensors' type;
+ *     y = t * (1 / sqrt(mean(t^2) + eps)) * (weight_offset + weight), in fp32.
+ * total_out receives t, y_out y rounded once, codes / scales the 8-bit form of the
+ * fp32 y.  Means, ranges and values that are not finite as for nvfp4_rmsnorm.
+ *
+ *   type            NVFP4_TYPE_BF16 or NVFP4_TYPE_FP16: x, residual, both weights,
+ *                   total_out and y_out.
+ *   x, residual     device [num_rows, ldx], [num_rows, ldr].
+ *   post            0 or 1.
+ *   post_weight, weight  device [K] or NULL (the factor is then 1, without offset).
+ *   gate            device [.., ldg] of gate_type (`type` or NVFP4_TYPE_FP32) or NULL
+ *                   (gate_scale alone): with gate_cols K one element per column
+ *                   (16-byte aligned, ldg * its size a multiple of 16), with 1 one
+ *                   per row, at gate[row * ldg]; ldg 0 for the same in every row.
+ *   gate_scale, residual_scale, weight_offset  finite; eps finite, >= 0.
+ *   K, y_out, fp8, codes, scales  as for nvfp4_rmsnorm.
+ *   total_out       device [num_rows, ldt] or NULL.
+ * Tensors of `type` are 16-byte aligned with strides that are multiples of 8.
+ * total_out and y_out may each be x or residual itself (same pointer and stride);
+ * outputs must not overlap anything in another way.  At least one output is needed.
+ * num_rows == 0 is a no-op.
+ */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* post_weight;
+  const void* weight;
+  const void* gate;
+  void* total_out;
+  void* y_out;
+  uint8_t* codes;
+  void* scales;
+  int64_t ldx, ldr, ldg, ldt, ldy;
+  int32_t num_rows, K;
+  int32_t type, post, gate_type, gate_cols, gate_act, fp8;
+  float weight_offset, eps, gate_scale, residual_scale;
+} nvfp4_block_norm_t;
+
+NVFP4_API nvfp4_status_t nvfp4_block_norm(const nvfp4_block_norm_t* p, nvfp4_stream_t stream);
+
 /* Activations of nvfp4_linear. */
 typedef enum {
   NVFP4_ACT_NONE = 0,
@@ -665,6 +719,29 @@ NVFP4_API nvfp4_status_t nvfp4_linear_workspace_size(const nvfp4_linear_t* p, si
  * has run.  The call only enqueues kernels and may be captured into a graph. */
 NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace,
                                       size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_combine — the last step of nvfp4_moe_forward as an operator of its own: the
+ * experts' rows back in token order, summed by routing weight,
+ *     out[t] = rnd(residual[t] + sum_j weights[t, j] * values[inv_pair[t * k + j]]),
+ * j ascending, in fp32, one rounding.  Pairs whose inv_pair is outside [0, num_rows) are
+ * left out of the sum.
+ *
+ *   type         of values: NVFP4_TYPE_BF16, FP16 or FP32; so residual_type, out_type.
+ *   values       device [num_rows, ldv].
+ *   weights      device fp32 [num_tokens, k];  inv_pair  device int32 [num_tokens * k].
+ *   residual     device [num_tokens, ldr] or NULL.
+ *   out          device [num_tokens, ldo]; may be residual itself (same pointer, type
+ *                and stride), must not overlap anything in another way.
+ *   H            elements per row, H % 8 == 0, at most 2^24;  1 <= k <= 1024.
+ * Tensors' rows are 16-byte aligned.  num_tokens == 0 is a no-op.
+ */
+NVFP4_API nvfp4_status_t nvfp4_combine(int32_t type, const void* values, int64_t ldv, int32_t num_rows,
+                                       const float* weights, const int32_t* inv_pair,
+                                       int32_t num_tokens, int32_t k, int32_t H,
+                                       int32_t residual_type, const void* residual, int64_t ldr,
+                                       int32_t out_type, void* out, int64_t ldo,
+                                       nvfp4_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -9,5 +9,6 @@ it to exist:
     from nvfp4_w4a4_expert_amd import _lib       # raw C entry points
     from nvfp4_w4a4_expert_amd import moe        # NVFP4MoELayer + weight prep
     from nvfp4_w4a4_expert_amd import dense      # norm, 8-bit rows and linear around the experts
+    from nvfp4_w4a4_expert_amd import experts    # routed experts in 16 or 8 bits, step by step
 """
-__all__ = ["build", "_lib", "moe", "dense"]
+__all__ = ["build", "_lib", "moe", "dense", "experts"]

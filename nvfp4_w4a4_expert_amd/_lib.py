@@ -75,10 +75,25 @@ class Linear(LinearFields):
                 _check_size(given, f"nvfp4_linear_t.{name}")
 
 
+class BlockNorm(ctypes.Structure):
+    """nvfp4_block_norm_t."""
+    _fields_ = [
+        ("x", _p), ("residual", _p), ("post_weight", _p), ("weight", _p), ("gate", _p),
+        ("total_out", _p), ("y_out", _p), ("codes", _p), ("scales", _p),
+        ("ldx", _i64), ("ldr", _i64), ("ldg", _i64), ("ldt", _i64), ("ldy", _i64),
+        ("num_rows", _i32), ("K", _i32),
+        ("type", _i32), ("post", _i32), ("gate_type", _i32), ("gate_cols", _i32),
+        ("gate_act", _i32), ("fp8", _i32),
+        ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
+        ("gate_scale", ctypes.c_float), ("residual_scale", ctypes.c_float),
+    ]
+
+
 _LINEAR_NAMES = tuple(name for name, _ in LinearFields._fields_)
 
 FP8_NONE = -1
 TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_FP8_ROW, TYPE_FP8_MX = range(5)
+GATE_PLAIN, GATE_SIGMOID, GATE_TANH = range(3)
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
 
 MOE_STAGES = ("route", "permute", "quantize_a1", "gemm1_w13", "gemm2_w2", "combine")
@@ -113,9 +128,12 @@ _SIGS = {
                                          ctypes.POINTER(MoEDebug), _p]),
     "nvfp4_rmsnorm": (_i32, [_i32, _p, _i64, _p, _i64, _p, ctypes.c_float, ctypes.c_float, _i32,
                              _i32, _p, _i64, _p, _i64, _i32, _p, _p, _p]),
+    "nvfp4_block_norm": (_i32, [ctypes.POINTER(BlockNorm), _p]),
     "nvfp4_quantize_rows_fp8": (_i32, [_i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
     "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(LinearFields), ctypes.POINTER(ctypes.c_size_t)]),
     "nvfp4_linear": (_i32, [ctypes.POINTER(LinearFields), _p, ctypes.c_size_t, _p]),
+    "nvfp4_combine": (_i32, [_i32, _p, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _i64, _i32,
+                             _p, _i64, _p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -329,6 +347,13 @@ def rmsnorm(*args):
         raise NVFP4Error(status, "nvfp4_rmsnorm")
 
 
+def block_norm(p: BlockNorm, stream):
+    """p's sizes are checked by the caller."""
+    status = _lib.nvfp4_block_norm(ctypes.byref(p), stream)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_block_norm")
+
+
 def quantize_rows_fp8(*args):
     """The arguments of nvfp4_quantize_rows_fp8, in order."""
     _check_size(args[3], "nvfp4_quantize_rows_fp8: num_rows")
@@ -349,3 +374,12 @@ def linear(p: LinearFields, workspace, workspace_bytes: int, stream):
     status = _lib.nvfp4_linear(ctypes.byref(p), workspace, workspace_bytes, stream)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_linear")
+
+
+def combine(*args):
+    """The arguments of nvfp4_combine, in order."""
+    for i, name in ((3, "num_rows"), (6, "num_tokens"), (7, "k"), (8, "H")):
+        _check_size(args[i], f"nvfp4_combine: {name}")
+    status = _lib.nvfp4_combine(*args)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_combine")

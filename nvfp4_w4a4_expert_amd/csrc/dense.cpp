@@ -1,5 +1,5 @@
 // C ABI of the dense operators around the routed experts: argument checking of
-// nvfp4_rmsnorm, nvfp4_quantize_rows_fp8 and nvfp4_linear.
+// nvfp4_rmsnorm, nvfp4_block_norm, nvfp4_quantize_rows_fp8, nvfp4_linear and nvfp4_combine.
 #include <math.h>
 #include <stdint.h>
 
@@ -90,6 +90,48 @@ NVFP4_API nvfp4_status_t nvfp4_rmsnorm(int32_t type, const void* x, int64_t ldx,
   return device_status(launch_rows(a, static_cast<hipStream_t>(stream)));
 }
 
+NVFP4_API nvfp4_status_t nvfp4_block_norm(const nvfp4_block_norm_t* p, nvfp4_stream_t stream) {
+  if (!p || (p->type != NVFP4_TYPE_BF16 && p->type != NVFP4_TYPE_FP16)) return NVFP4_ERR_INVALID_ARG;
+  if (p->fp8 != NVFP4_FP8_NONE && !is_fp8(p->fp8)) return NVFP4_ERR_INVALID_ARG;
+  const int32_t K = p->K;
+  if (p->num_rows < 0 || K < 8 || K % 8 || (p->fp8 == NVFP4_TYPE_FP8_MX && K % 32)) return NVFP4_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.0f) || !isfinite(p->eps) || !isfinite(p->weight_offset) || !isfinite(p->gate_scale) ||
+      !isfinite(p->residual_scale) || (p->post != 0 && p->post != 1))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->gate) {
+    if (p->gate_type != p->type && p->gate_type != NVFP4_TYPE_FP32) return NVFP4_ERR_INVALID_ARG;
+    if (p->gate_act < NVFP4_GATE_PLAIN || p->gate_act > NVFP4_GATE_TANH) return NVFP4_ERR_INVALID_ARG;
+    if ((p->gate_cols != 1 && p->gate_cols != K) || p->ldg < 0) return NVFP4_ERR_INVALID_ARG;
+  }
+  if (K > kRowsMaxK) return NVFP4_ERR_UNSUPPORTED;
+  if (p->num_rows == 0) return NVFP4_OK;
+  if (!p->x || !p->residual || bad_rows(p->x, p->ldx, K) || bad_rows(p->residual, p->ldr, K) ||
+      (p->post_weight && !aligned(p->post_weight, 16)) || (p->weight && !aligned(p->weight, 16)) ||
+      (p->total_out && bad_rows(p->total_out, p->ldt, K)) || (p->y_out && bad_rows(p->y_out, p->ldy, K)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->gate) {
+    const int64_t size = float_size(p->gate_type);
+    if (!aligned(p->gate, p->gate_cols == 1 ? size : 16)) return NVFP4_ERR_INVALID_ARG;
+    if (p->gate_cols != 1 && (p->ldg * size % 16 || (p->ldg != 0 && p->ldg < K))) return NVFP4_ERR_INVALID_ARG;
+  }
+  if (!p->total_out && !p->y_out && p->fp8 == NVFP4_FP8_NONE) return NVFP4_ERR_INVALID_ARG;
+  if (p->fp8 != NVFP4_FP8_NONE) {
+    const nvfp4_status_t st = check_fp8_out(p->fp8, K, p->codes, p->scales);
+    if (st != NVFP4_OK) return st;
+  }
+  BlockArgs a = {};
+  a.x = p->x; a.residual = p->residual; a.post_weight = p->post_weight; a.weight = p->weight; a.gate = p->gate;
+  a.total_out = p->total_out; a.y_out = p->y_out; a.codes = p->codes; a.scales = p->scales;
+  a.ldx = p->ldx; a.ldr = p->ldr; a.ldg = p->ldg; a.ldt = p->ldt; a.ldy = p->ldy;
+  a.rows = p->num_rows; a.K = K;
+  a.fp8 = p->fp8 == NVFP4_FP8_NONE ? 0 : p->fp8 == NVFP4_TYPE_FP8_ROW ? 1 : 2;
+  a.gate_act = p->gate ? p->gate_act : 0;
+  a.offset = p->weight_offset; a.eps = p->eps; a.gate_scale = p->gate_scale; a.residual_scale = p->residual_scale;
+  a.fp16 = p->type == NVFP4_TYPE_FP16; a.post = p->post != 0;
+  a.gate_wide = p->gate && p->gate_cols != 1; a.gate_f32 = p->gate && p->gate_type == NVFP4_TYPE_FP32;
+  return device_status(launch_block(a, static_cast<hipStream_t>(stream)));
+}
+
 NVFP4_API nvfp4_status_t nvfp4_quantize_rows_fp8(int32_t type, const void* x, int64_t ldx, int32_t num_rows,
                                                  int32_t K, int32_t fp8, uint8_t* codes, void* scales,
                                                  nvfp4_stream_t stream) {
@@ -150,6 +192,29 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, 
   const size_t need = linear_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return NVFP4_ERR_WORKSPACE;
   return device_status(launch_linear(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+NVFP4_API nvfp4_status_t nvfp4_combine(int32_t type, const void* values, int64_t ldv, int32_t num_rows,
+                                       const float* weights, const int32_t* inv_pair, int32_t num_tokens, int32_t k,
+                                       int32_t H, int32_t residual_type, const void* residual, int64_t ldr,
+                                       int32_t out_type, void* out, int64_t ldo, nvfp4_stream_t stream) {
+  if (!is_float_type(type) || !is_float_type(out_type) || (residual && !is_float_type(residual_type)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (num_rows < 0 || num_tokens < 0 || k < 1 || H < 8 || H % 8) return NVFP4_ERR_INVALID_ARG;
+  if (H > (1 << 24) || k > 1024) return NVFP4_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return NVFP4_OK;
+  auto bad = [&](const void* p, int64_t ld, int32_t t) {
+    return !p || !aligned(p, 16) || ld < H || ld * (int64_t)float_size(t) % 16;
+  };
+  if ((num_rows > 0 && bad(values, ldv, type)) || bad(out, ldo, out_type) || (residual && bad(residual, ldr, residual_type)) ||
+      !weights || !inv_pair || !aligned(weights, 4) || !aligned(inv_pair, 4))
+    return NVFP4_ERR_INVALID_ARG;
+  CombineArgs a = {};
+  a.values = values; a.weights = weights; a.inv = inv_pair; a.residual = residual; a.out = out;
+  a.ldv = ldv; a.ldr = ldr; a.ldo = ldo;
+  a.rows = num_rows; a.T = num_tokens; a.k = k; a.H = H;
+  a.type = elem_type(type); a.residual_type = elem_type(residual_type); a.out_type = elem_type(out_type);
+  return device_status(launch_combine_rows(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -106,6 +106,18 @@ hipError_t launch_combine(const float* c2, const float* w, const int32_t* inv, i
                           int32_t k, int32_t H, const uint16_t* residual, uint16_t* out,
                           hipStream_t stream);
 
+// The combine as an operator of its own.  Types: 0 bf16, 1 fp16, 2 fp32.
+struct CombineArgs {
+  const void* values;       // [rows, ldv]
+  const float* weights;     // [T, k]
+  const int32_t* inv;       // [T, k]: rows of values; others are left out
+  const void* residual;     // [T, ldr] or null
+  void* out;                // [T, ldo]
+  int64_t ldv, ldr, ldo;
+  int32_t rows, T, k, H, type, residual_type, out_type;
+};
+hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t stream);
+
 // Row operators of the dense half (rows.hip).  fp8: 0 none, 1 one fp32 scale
 // per row, 2 one UE8M0 scale per 32 elements.
 constexpr int32_t kRowsMaxK = 32768;
@@ -123,6 +135,24 @@ struct RowArgs {
   bool fp16, norm;
 };
 hipError_t launch_rows(const RowArgs& a, hipStream_t stream);
+
+// The norms around a block with its gate and residual (block.hip).  fp8 as above.
+struct BlockArgs {
+  const void* x;
+  const void* residual;
+  const void* post_weight;  // or null
+  const void* weight;       // or null
+  const void* gate;         // or null; [rows or 1, K or 1] by ldg and gate_wide
+  void* total_out;          // or null
+  void* y_out;              // or null
+  uint8_t* codes;           // null when fp8 == 0
+  void* scales;
+  int64_t ldx, ldr, ldg, ldt, ldy;
+  int32_t rows, K, fp8, gate_act;   // gate_act: 0 none, 1 sigmoid, 2 tanh
+  float offset, eps, gate_scale, residual_scale;
+  bool fp16, post, gate_wide, gate_f32;
+};
+hipError_t launch_block(const BlockArgs& a, hipStream_t stream);
 
 // The dense linear operator (linear.hip).  kind: 0 bf16, 1 fp16, 2 E4M3 with
 // fp32 row scales, 3 E4M3 with UE8M0 block scales.  Element types of bias,

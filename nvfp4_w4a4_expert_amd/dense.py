@@ -1,7 +1,7 @@
 """The dense operators around the routed experts, on torch tensors.
 
 ``rms_norm`` adds the residual, normalises and quantises in one pass,
-``quantize_fp8`` makes the same 8-bit form of given rows, ``linear`` is a
+``block_norm`` does so behind a block's own last norm and gate, ``quantize_fp8`` makes the same 8-bit form of given rows, ``linear`` is a
 matrix product with bias, activation (plain or gated) and residual in its
 epilogue, on bf16, fp16 or 8-bit operands.  A dense feed-forward beside the
 experts, in 8 bits end to end:
@@ -250,6 +250,119 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
             codes_at, scales_at = fp8.codes.data_ptr(), fp8.scales.data_ptr()
         _lib.rmsnorm(_TYPES[dtype], x_at, ldx, r_at, ldr, w_at, weight_offset, eps, T, K,
                      total_at, lds, y_at, ldy, kind, codes_at, scales_at, handle)
+    return NormOut(out, total_out, fp8)
+
+
+_GATE_ACTS = {None: _lib.GATE_PLAIN, "none": _lib.GATE_PLAIN, "sigmoid": _lib.GATE_SIGMOID,
+              "tanh": _lib.GATE_TANH}
+
+
+def _gate(gate, T, K, dtype):
+    """(address, row stride, columns, type) of a gate tensor that broadcasts to [T, K]."""
+    if gate.layout is not torch.strided or gate.dtype not in (dtype, torch.float32) or \
+            gate.dim() not in (1, 2) or gate.shape[-1] not in (1, K) or \
+            (gate.dim() == 2 and gate.shape[0] not in (1, T)):
+        raise ValueError(f"gate must be a number or a {dtype} or fp32 tensor of [1], [{K}], [1, {K}], "
+                         f"[{T}, 1] or [{T}, {K}]")
+    st = gate.stride()
+    ld = st[0] if gate.dim() == 2 and gate.shape[0] == T and T > 1 else 0
+    wide = gate.shape[-1] == K
+    if wide and T and (st[-1] != 1 or gate.data_ptr() % 16 or ld * gate.element_size() % 16 or 0 < ld < K):
+        raise ValueError("gate's rows must be contiguous and start on 16-byte boundaries")
+    return gate.data_ptr(), ld, K if wide else 1, _TYPES[gate.dtype]
+
+
+def _weight(w, name, K, dtype):
+    """The address of a norm's weight, checked."""
+    if w is None:
+        return None
+    if not (isinstance(w, torch.Tensor) and w.dtype == dtype and w.shape == (K,) and
+            w.is_contiguous() and w.data_ptr() % 16 == 0):
+        raise ValueError(f"{name} must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
+    return w.data_ptr()
+
+
+def block_norm(x: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = True,
+               post_weight: Optional[torch.Tensor] = None,
+               gate: Union[torch.Tensor, float, None] = None, gate_act: Optional[str] = None,
+               residual_scale: float = 1.0, weight: Optional[torch.Tensor] = None,
+               eps: float = 1e-6, weight_offset: float = 0.0, want_y: bool = True,
+               scales: Optional[str] = None, out: Optional[torch.Tensor] = None,
+               total_out: Optional[torch.Tensor] = None, stream=None) -> NormOut:
+    """A block's end and the next one's start in one pass: nvfp4_block_norm.
+
+        b = x / sqrt(mean(x^2) + eps) * (weight_offset + post_weight)   (x without post_norm)
+        total = residual_scale * residual + gate * b                    (rounded to x's type)
+        y = total / sqrt(mean(total^2) + eps) * (weight_offset + weight)
+
+    x (the block's output) and residual [rows, K] bf16 or fp16 with K a multiple
+    of 8, at most 32768; both weights [K] of x's type (the factor is 1 without).
+    gate: a number, or a tensor of x's type or fp32, one element per row
+    ([rows, 1]), per column ([K] or [1, K]), per element ([rows, K]) or one for
+    all ([1]), through gate_act: None, "sigmoid" or "tanh" (tensors only).
+    Returns NormOut(y, total, fp8) as rms_norm does, total always (into
+    `total_out`, which like `out` may be x or residual); without want_y and
+    scales only the total is computed."""
+    T, K, ldx, x_at = _rows(x, "x")
+    _check_K(K)
+    dtype = x.dtype
+    _, _, ldr, r_at = _rows(residual, "residual", K, T, (dtype,))
+    if not (post_norm is True or post_norm is False):
+        raise ValueError("post_norm must be True or False")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    p_at, w_at = _weight(post_weight, "post_weight", K, dtype), _weight(weight, "weight", K, dtype)
+    if weight is not None and not want_y and scales is None:
+        raise ValueError("weight needs want_y or scales")
+    try:
+        act = _GATE_ACTS[gate_act]
+    except (KeyError, TypeError):
+        raise ValueError(f"gate_act must be one of {[k for k in _GATE_ACTS]}, not {gate_act!r}") from None
+    g_at, ldg, gate_cols, gate_type, gate_scale = None, 0, 0, 0, 1.0
+    gate_t = gate if isinstance(gate, torch.Tensor) else None
+    if gate_t is not None:
+        g_at, ldg, gate_cols, gate_type = _gate(gate, T, K, dtype)
+    elif act:
+        raise ValueError("gate_act needs a gate tensor")
+    elif gate is not None:
+        try:
+            gate_scale = float(gate)
+        except (TypeError, ValueError):
+            raise ValueError("gate must be a number or a tensor") from None
+    if scales is not None:
+        _check_scales(scales, K)
+    eps, weight_offset, residual_scale = float(eps), float(weight_offset), float(residual_scale)
+    if not (0.0 <= eps < 3.4e38 and -3.4e38 < weight_offset < 3.4e38 and
+            -3.4e38 < gate_scale < 3.4e38 and -3.4e38 < residual_scale < 3.4e38):
+        raise ValueError("eps must be finite and >= 0, weight_offset, gate and residual_scale finite")
+    y_at = codes_at = scales_at = None
+    ldy = ldt = K
+    if out is not None:
+        _need(want_y, "out needs want_y")
+        _, _, ldy, y_at = _rows(out, "out", K, T, (dtype,))
+        _check_apart(out, "out", (post_weight, weight, gate_t, total_out))
+        _check_apart(out, "out", (x, residual), True)
+    if total_out is not None:
+        _, _, ldt, t_at = _rows(total_out, "total_out", K, T, (dtype,))
+        _check_apart(total_out, "total_out", (post_weight, weight, gate_t))
+        _check_apart(total_out, "total_out", (x, residual), True)
+    handle, ctx = _on((x, residual, post_weight, weight, gate_t, out, total_out), stream)
+    with ctx:
+        fp8, kind = None, _lib.FP8_NONE
+        if want_y and out is None:
+            out = _empty(T, K, dtype)
+            y_at = out.data_ptr()
+        if total_out is None:
+            total_out = _empty(T, K, dtype)
+            t_at = total_out.data_ptr()
+        if scales is not None:
+            kind = _FP8[scales]
+            fp8 = _fp8_out(T, K, scales)
+            codes_at, scales_at = fp8.codes.data_ptr(), fp8.scales.data_ptr()
+        _lib.block_norm(_lib.BlockNorm(
+            x_at, r_at, p_at, w_at, g_at, t_at, y_at, codes_at, scales_at, ldx, ldr, ldg, ldt, ldy,
+            T, K, _TYPES[dtype], post_norm, gate_type, gate_cols, act, kind,
+            weight_offset, eps, gate_scale, residual_scale), handle)
     return NormOut(out, total_out, fp8)
 
 

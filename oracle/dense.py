@@ -118,6 +118,41 @@ def rms_norm(s, weight, eps, offset):
     return y, np.abs(y) * 36 * U + 2.0 ** -148
 
 
+def block_total(x, residual, post, post_weight, eps, offset, gate, act, residual_scale):
+    """(t, fp32 error bound) of residual_scale * residual + act(gate) * b, b the norm of
+    x or x.  gate: a number or an array that broadcasts.  A sigmoid takes an exponential
+    (2 u of its value, and 0 below 2^-126), a sum and a quotient, a tanh is off by 2
+    steps: 8 u cover either, and the products with gate and number."""
+    b, be = rms_norm(x, post_weight, eps, offset) if post else (np.asarray(x, dtype=np.float64), 0.0)
+    g = np.asarray(gate, dtype=np.float64)
+    if act == "sigmoid":
+        g = 1 / (1 + np.exp(-g))
+    elif act == "tanh":
+        g = np.tanh(g)
+    with np.errstate(all="ignore"):
+        r = residual_scale * np.asarray(residual, dtype=np.float64)
+        t = r + g * b
+        err = np.abs(g) * be + 10 * U * np.abs(g * b) + 2.0 ** -125 * np.abs(b) + 2 * U * np.abs(r) + U * np.abs(t) + 2.0 ** -148
+    return t, err
+
+
+def combine(values, weights, inv, residual=None):
+    """(out, fp32 error bound): k products and sums in order, then the residual."""
+    T, k = weights.shape
+    out, mags = np.zeros((T, values.shape[1])), np.zeros((T, values.shape[1]))
+    place = np.asarray(inv).reshape(T, k)
+    for j in range(k):
+        ok = (place[:, j] >= 0) & (place[:, j] < values.shape[0])
+        p = values[np.where(ok, place[:, j], 0)] * weights[:, j:j + 1].astype(np.float64)
+        out += np.where(ok[:, None], p, 0)
+        mags += np.where(ok[:, None], np.abs(p), 0)
+    err = (k + 1) * U * mags + k * 2.0 ** -149
+    if residual is not None:
+        out = out + residual
+        err = err + U * (mags + np.abs(residual))
+    return out, err
+
+
 # ---- linear --------------------------------------------------------------------
 
 def activate(v, act):
