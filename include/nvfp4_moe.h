@@ -721,6 +721,58 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace,
                                       size_t workspace_bytes, nvfp4_stream_t stream);
 
 /*
+ * ---- The routed experts in 16 or 8 bits, step by step --------------------------
+ * nvfp4_route_topk and nvfp4_permute above, then the products, then the combine.
+ */
+
+/*
+ * nvfp4_grouped_linear — nvfp4_linear for rows grouped by expert: row m of the result
+ * with offsets[e] <= m < offsets[e + 1] is
+ *     out[m, n] = act(v[n]) or, gated, act(v[n]) * v[N + n],
+ *     v[n]      = sum_k a[row(m), k] * w[e, n, k] (+ bias[e, n]),
+ *     row(m)    = index ? index[m] / index_div : m.
+ * Groups may have any size, none among them.  Rows of the result outside
+ * [offsets[0], offsets[num_experts]) are not written, nor those whose index is outside
+ * [0, a_rows * index_div).  An offset counts as the largest of those up to it, held in
+ * [0, num_rows]: offsets out of order or range leave groups empty and lead nowhere else.
+ * Accumulation, rounding, types and the 8-bit forms' products as for nvfp4_linear: a
+ * mean of at most 16 rows for each expert (of those that num_rows rows can reach) takes
+ * the exact products, more may take the scaled instruction where that does.
+ *
+ *   a            device [a_rows, lda] of `type`; a_rows >= num_rows without an index.
+ *   w            device [num_experts, N or 2N, ldw], w_each elements from one expert to
+ *                the next; alignment and strides as for nvfp4_linear, w_each * its
+ *                element size a multiple of 16.
+ *   a_scales     float [a_rows] or uint8 [a_rows, K/32];  w_scales  float [num_experts,
+ *                rows] or uint8 [num_experts, rows, K/32], contiguous.
+ *   bias         device [num_experts, N or 2N] of bias_type, contiguous, or NULL.
+ *   offsets      device int32 [num_experts + 1];  1 <= num_experts <= 1024.
+ *   index        device int32 [num_rows] or NULL;  index_div >= 1 (read with an index).
+ *   out          device [num_rows, ldo] of out_type, out_scales as for nvfp4_linear.
+ * out must not overlap any input.  num_rows == 0, a_rows == 0 or N == 0 is a no-op.
+ * K <= 2^22, N <= 2^24, num_rows <= 2^29, row strides of a and w <= 2^23 bytes and one
+ * launch of tiles (NVFP4_ERR_UNSUPPORTED else).  No workspace; may be captured.
+ */
+typedef struct {
+  const void* a;
+  const void* a_scales;
+  const void* w;
+  const void* w_scales;
+  const void* bias;
+  const int32_t* offsets;
+  const int32_t* index;
+  void* out;
+  uint8_t* out_scales;
+  int64_t lda, ldw, w_each, ldo;
+  int32_t num_rows, a_rows, num_experts, N, K, index_div;
+  int32_t type, bias_type, out_type;
+  int32_t act;              /* NVFP4_ACT_* */
+  int32_t gated;            /* 0 or 1 */
+} nvfp4_grouped_linear_t;
+
+NVFP4_API nvfp4_status_t nvfp4_grouped_linear(const nvfp4_grouped_linear_t* p, nvfp4_stream_t stream);
+
+/*
  * nvfp4_combine — the last step of nvfp4_moe_forward as an operator of its own: the
  * experts' rows back in token order, summed by routing weight,
  *     out[t] = rnd(residual[t] + sum_j weights[t, j] * values[inv_pair[t * k + j]]),

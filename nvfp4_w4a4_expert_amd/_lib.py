@@ -89,6 +89,18 @@ class BlockNorm(ctypes.Structure):
     ]
 
 
+class GroupedLinear(ctypes.Structure):
+    """nvfp4_grouped_linear_t."""
+    _fields_ = [
+        ("a", _p), ("a_scales", _p), ("w", _p), ("w_scales", _p), ("bias", _p),
+        ("offsets", _p), ("index", _p), ("out", _p), ("out_scales", _p),
+        ("lda", _i64), ("ldw", _i64), ("w_each", _i64), ("ldo", _i64),
+        ("num_rows", _i32), ("a_rows", _i32), ("num_experts", _i32), ("N", _i32), ("K", _i32),
+        ("index_div", _i32), ("type", _i32), ("bias_type", _i32), ("out_type", _i32),
+        ("act", _i32), ("gated", _i32),
+    ]
+
+
 _LINEAR_NAMES = tuple(name for name, _ in LinearFields._fields_)
 
 FP8_NONE = -1
@@ -132,6 +144,7 @@ _SIGS = {
     "nvfp4_quantize_rows_fp8": (_i32, [_i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
     "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(LinearFields), ctypes.POINTER(ctypes.c_size_t)]),
     "nvfp4_linear": (_i32, [ctypes.POINTER(LinearFields), _p, ctypes.c_size_t, _p]),
+    "nvfp4_grouped_linear": (_i32, [ctypes.POINTER(GroupedLinear), _p]),
     "nvfp4_combine": (_i32, [_i32, _p, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _i64, _i32,
                              _p, _i64, _p]),
 }
@@ -374,6 +387,13 @@ def linear(p: LinearFields, workspace, workspace_bytes: int, stream):
     status = _lib.nvfp4_linear(ctypes.byref(p), workspace, workspace_bytes, stream)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_linear")
+
+
+def grouped_linear(p: GroupedLinear, stream):
+    """p's sizes are checked by the caller."""
+    status = _lib.nvfp4_grouped_linear(ctypes.byref(p), stream)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_grouped_linear")
 
 
 def combine(*args):

@@ -21,10 +21,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libnvfp4moe.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
-JOBS = 4                      # compilers at once
+JOBS = 6                      # compilers at once
 
 SOURCES = ["api.cpp", "quant.hip", "route.hip", "gemm.hip", "combine.hip", "noalloc.hip",
-           "dense.cpp", "rows.hip", "block.hip", "linear.hip"]
+           "dense.cpp", "rows.hip", "block.hip", "linear.hip", "grouped.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1,5 +1,6 @@
 // C ABI of the dense operators around the routed experts: argument checking of
-// nvfp4_rmsnorm, nvfp4_block_norm, nvfp4_quantize_rows_fp8, nvfp4_linear and nvfp4_combine.
+// nvfp4_rmsnorm, nvfp4_block_norm, nvfp4_quantize_rows_fp8, nvfp4_linear, nvfp4_grouped_linear
+// and nvfp4_combine.
 #include <math.h>
 #include <stdint.h>
 
@@ -34,22 +35,30 @@ int32_t elem_type(int32_t t) {
   return t == NVFP4_TYPE_BF16 ? 0 : t == NVFP4_TYPE_FP16 ? 1 : t == NVFP4_TYPE_FP32 ? 2 : 3;
 }
 
+// Types and sizes that nvfp4_linear and nvfp4_grouped_linear share.
+bool bad_product(int32_t type, int32_t out_type, int32_t act, int32_t gated, int32_t N, int32_t K) {
+  if (N < 0 || K < 1) return true;
+  if (type != NVFP4_TYPE_BF16 && type != NVFP4_TYPE_FP16 && !is_fp8(type)) return true;
+  if (K % (type == NVFP4_TYPE_FP8_MX ? 32 : is_fp8(type) ? 16 : 8)) return true;
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_RELU || (gated != 0 && gated != 1)) return true;
+  if (!is_float_type(out_type) && out_type != NVFP4_TYPE_FP8_MX) return true;
+  return out_type == NVFP4_TYPE_FP8_MX && N % 32;
+}
+
+int32_t operand_kind(int32_t t) {
+  return t == NVFP4_TYPE_BF16 ? 0 : t == NVFP4_TYPE_FP16 ? 1 : t == NVFP4_TYPE_FP8_ROW ? 2 : 3;
+}
+
 // Sizes and types alone (no pointer of *p is looked at), as nvfp4_linear_workspace_size
 // and nvfp4_linear both need them.
 nvfp4_status_t check_linear_sizes(const nvfp4_linear_t* p, LinearArgs* a) {
-  if (!p || p->M < 0 || p->N < 0 || p->K < 1) return NVFP4_ERR_INVALID_ARG;
-  if (p->type != NVFP4_TYPE_BF16 && p->type != NVFP4_TYPE_FP16 && !is_fp8(p->type)) return NVFP4_ERR_INVALID_ARG;
-  if (p->K % (p->type == NVFP4_TYPE_FP8_MX ? 32 : is_fp8(p->type) ? 16 : 8)) return NVFP4_ERR_INVALID_ARG;
-  if (p->act < NVFP4_ACT_NONE || p->act > NVFP4_ACT_RELU || (p->gated != 0 && p->gated != 1))
-    return NVFP4_ERR_INVALID_ARG;
-  if (!is_float_type(p->out_type) && p->out_type != NVFP4_TYPE_FP8_MX) return NVFP4_ERR_INVALID_ARG;
-  if (p->out_type == NVFP4_TYPE_FP8_MX && p->N % 32) return NVFP4_ERR_INVALID_ARG;
+  if (!p || p->M < 0 || bad_product(p->type, p->out_type, p->act, p->gated, p->N, p->K)) return NVFP4_ERR_INVALID_ARG;
   // 32-bit sizes inside the kernels: a tile's offsets, rows of w, tiles of a launch
   if (p->K > (1 << 22) || p->N > (1 << 24)) return NVFP4_ERR_UNSUPPORTED;
   const int64_t tiles = (((int64_t)p->M + 255) / 256) * (((int64_t)p->N * (p->gated + 1) + 255) / 256);
   if (tiles > (1 << 20)) return NVFP4_ERR_UNSUPPORTED;
   a->M = p->M; a->N = p->N; a->K = p->K;
-  a->kind = p->type == NVFP4_TYPE_BF16 ? 0 : p->type == NVFP4_TYPE_FP16 ? 1 : p->type == NVFP4_TYPE_FP8_ROW ? 2 : 3;
+  a->kind = operand_kind(p->type);
   a->act = p->act; a->gated = p->gated;
   a->out_type = elem_type(p->out_type);
   return NVFP4_OK;
@@ -192,6 +201,42 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, 
   const size_t need = linear_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return NVFP4_ERR_WORKSPACE;
   return device_status(launch_linear(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+NVFP4_API nvfp4_status_t nvfp4_grouped_linear(const nvfp4_grouped_linear_t* p, nvfp4_stream_t stream) {
+  if (!p || p->num_rows < 0 || p->a_rows < 0 || p->num_experts < 1 ||
+      bad_product(p->type, p->out_type, p->act, p->gated, p->N, p->K))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->index ? p->index_div < 1 : p->a_rows < p->num_rows) return NVFP4_ERR_INVALID_ARG;
+  if (p->bias && !is_float_type(p->bias_type)) return NVFP4_ERR_INVALID_ARG;
+  if (p->num_experts > 1024 || p->K > (1 << 22) || p->N > (1 << 24) || p->num_rows > (1 << 29)) return NVFP4_ERR_UNSUPPORTED;
+  GroupedArgs a = {};
+  a.M = p->num_rows; a.a_rows = p->a_rows; a.experts = p->num_experts; a.N = p->N; a.K = p->K; a.index_div = p->index_div;
+  a.kind = operand_kind(p->type); a.act = p->act; a.gated = p->gated; a.out_type = elem_type(p->out_type);
+  if (!grouped_fits(a)) return NVFP4_ERR_UNSUPPORTED;
+  if (p->num_rows == 0 || p->a_rows == 0 || p->N == 0) return NVFP4_OK;
+  const bool f8 = is_fp8(p->type);
+  const int64_t esz = f8 ? 1 : 2, rows = (int64_t)p->N * (p->gated + 1);
+  if (!p->a || !p->w || !p->out || !p->offsets || !aligned(p->a, 16) || !aligned(p->w, 16) || !aligned(p->offsets, 4) ||
+      !aligned(p->index, 4))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->lda < p->K || p->ldw < p->K || p->lda * esz % 16 || p->ldw * esz % 16) return NVFP4_ERR_INVALID_ARG;
+  if (p->lda * esz > (1 << 23) || p->ldw * esz > (1 << 23)) return NVFP4_ERR_UNSUPPORTED;
+  if (p->num_experts > 1 && (p->w_each * esz % 16 || p->w_each < (rows - 1) * p->ldw + p->K)) return NVFP4_ERR_INVALID_ARG;
+  if (f8 && (!p->a_scales || !p->w_scales)) return NVFP4_ERR_INVALID_ARG;
+  if (p->type == NVFP4_TYPE_FP8_ROW && (!aligned(p->a_scales, 4) || !aligned(p->w_scales, 4))) return NVFP4_ERR_INVALID_ARG;
+  if (p->bias && !aligned(p->bias, float_size(p->bias_type))) return NVFP4_ERR_INVALID_ARG;
+  if (p->ldo < p->N) return NVFP4_ERR_INVALID_ARG;
+  if (p->out_type == NVFP4_TYPE_FP8_MX) {
+    if (!p->out_scales || !aligned(p->out, 16) || p->ldo % 16) return NVFP4_ERR_INVALID_ARG;
+  } else if (!aligned(p->out, float_size(p->out_type))) {
+    return NVFP4_ERR_INVALID_ARG;
+  }
+  a.a = p->a; a.a_scales = p->a_scales; a.w = p->w; a.w_scales = p->w_scales; a.bias = p->bias;
+  a.offsets = p->offsets; a.index = p->index; a.out = p->out; a.out_scales = p->out_scales;
+  a.lda = p->lda; a.ldw = p->ldw; a.w_each = p->num_experts > 1 ? p->w_each : 0; a.ldo = p->ldo;
+  a.bias_type = elem_type(p->bias_type);
+  return device_status(launch_grouped(a, static_cast<hipStream_t>(stream)));
 }
 
 NVFP4_API nvfp4_status_t nvfp4_combine(int32_t type, const void* values, int64_t ldv, int32_t num_rows,

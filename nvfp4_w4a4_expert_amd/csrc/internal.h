@@ -172,6 +172,24 @@ struct LinearArgs {
   int32_t kind, act, gated, bias_type, residual_type, out_type;
 };
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream);
+
+// The same product for rows grouped by expert (grouped.hip).
+struct GroupedArgs {
+  const void* a;            // [a_rows, lda]
+  const void* a_scales;
+  const void* w;            // [experts, N or 2N, ldw], w_each elements between experts
+  const void* w_scales;     // [experts, N or 2N (, K/32)]
+  const void* bias;         // [experts, N or 2N] or null
+  const int32_t* offsets;   // [experts + 1]
+  const int32_t* index;     // [M] or null: row m multiplies row index[m] / index_div of a
+  void* out;                // [M, ldo]
+  uint8_t* out_scales;      // [M, N/32] (out type 3)
+  int64_t lda, ldw, w_each, ldo;
+  int32_t M, a_rows, experts, N, K, index_div;
+  int32_t kind, act, gated, bias_type, out_type;
+};
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+bool grouped_fits(const GroupedArgs& a);              // one launch holds it (reads sizes, kind, out_type and gated)
 size_t linear_workspace_bytes(const LinearArgs& a);   // reads sizes, kind, out_type and gated
 
 }  // namespace nvfp4

@@ -98,6 +98,26 @@ inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) 
   return best;
 }
 
+// The kernel of a product grouped by expert: M rows over `experts` groups of sizes that
+// only the device knows.  row_tiles is the most tiles (of 16 rows for the few-row form)
+// that M rows can fall into; tiles beyond those in use end at once.
+struct GroupPlan {
+  int kernel;
+  int32_t tile, tiles_n;
+  int64_t row_tiles;
+};
+
+inline GroupPlan group_plan_of(int32_t M, int32_t experts, int32_t N, int32_t kbytes, int kind, bool gated, int out_type) {
+  const int32_t groups = M < experts ? M : experts, mean = M / groups;
+  GroupPlan q;
+  q.kernel = mean <= 16 ? kFew : mean <= 96 ? kTile64 : kTile128;
+  q.tile = q.kernel == kFew ? 16 : q.kernel == kTile64 ? 64 : 128;
+  const int32_t columns = q.kernel == kFew ? (out_type == kOutBlock8 ? 32 : 16) : gated ? q.tile / 2 : q.tile;
+  q.tiles_n = (N - 1) / columns + 1;
+  q.row_tiles = (int64_t)(M - groups) / q.tile + groups;
+  return q;
+}
+
 // 8-bit operands: the exact instructions where fp32's accuracy shows in the output
 // (fp32 itself; block scales, which change by a factor of two at a border) and where
 // reading w is the bound anyway.

@@ -5,19 +5,22 @@ experts that are held in 16 or 8 bits:
 
     r = route(logits, k)                                   # ids, weights
     g = permute(r.ids, num_experts)                        # rows grouped by expert
-    y = combine(rows_by_expert, r.weights, g.inv_pair, residual=h)
+    h = grouped_linear(x, w13, g.offsets, index=g.src_pair, index_div=k, act="silu", gated=True)
+    v = grouped_linear(h, w2, g.offsets, out_dtype=torch.float32)
+    y = combine(v, r.weights, g.inv_pair, residual=x)
 
-Conventions (ValueError for what does not fit, streams, memory, graphs, no
+``ExpertsLayer`` holds a layer's weights and runs these.  Conventions (ValueError for what does not fit, streams, memory, graphs, no
 gradients) are those of ``dense``.
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Union
 
 import torch
 
 from . import _lib
-from .dense import _FLOATS, _TYPES, _check_apart, _empty, _empty_strided, _need, _on, _rows
+from .dense import (_ACTS, _FLOATS, _TYPES, FP8Rows, Operand, _check_apart, _empty, _empty_strided, _fp8_out, _need, _on,
+                    _operand, _plain, _rows, quantize_fp8)
 
 
 class Routing(NamedTuple):
@@ -81,6 +84,115 @@ def permute(ids: torch.Tensor, num_experts: int, *, stream=None) -> Grouping:
     return out
 
 
+def _expert_weights(w, kind, a_name):
+    """(experts, rows, K, row stride, expert stride, values, scales) of a grouped
+    product's weights, checked; kind is a's."""
+    scales = None
+    if kind in (_lib.TYPE_FP8_ROW, _lib.TYPE_FP8_MX):
+        _need(isinstance(w, tuple) and len(w) == 2, f"w must be an FP8Rows, as {a_name}")
+        w, scales = w
+        dtype = torch.uint8
+    else:
+        dtype = torch.bfloat16 if kind == _lib.TYPE_BF16 else torch.float16
+    _need(isinstance(w, torch.Tensor) and w.dtype == dtype and w.dim() == 3 and w.layout is torch.strided,
+          f"w must be a {str(dtype).replace('torch.', '')} [experts, rows, K] tensor, as {a_name}")
+    E, rows, K = w.shape
+    _need(1 <= E <= 1024, f"w must hold between 1 and 1024 experts, not {E}")
+    per16 = 16 // w.element_size()
+    each, ld, step = w.stride()
+    if rows <= 1:
+        ld = -(-K // per16) * per16
+    if E == 1:
+        each = 0
+    if rows and K and ((step != 1 and K != 1) or ld < K or ld % per16 or each % per16 or w.data_ptr() % 16 or
+                       (E > 1 and each < (rows - 1) * ld + K)):
+        raise ValueError("w's rows must be contiguous, apart and start on 16-byte boundaries")
+    if scales is not None:
+        shape, dtype = ((E, rows), torch.float32) if kind == _lib.TYPE_FP8_ROW else ((E, rows, K // 32), torch.uint8)
+        _vector(scales, "w's scales", dtype, (shape,))
+    return E, rows, K, ld, each, w, scales
+
+
+def grouped_linear(a: Operand, w: Operand, offsets: torch.Tensor, *, index: Optional[torch.Tensor] = None,
+                   index_div: int = 1, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
+                   gated: bool = False, out_dtype: Union[torch.dtype, str, None] = None,
+                   out: Optional[torch.Tensor] = None, stream=None) -> Operand:
+    """dense.linear for rows grouped by expert, each group with its own weight:
+    nvfp4_grouped_linear.  Row m with offsets[e] <= m < offsets[e + 1] is
+
+        act(a[row(m)] . w[e]^T + bias[e])     or     act(gate) * up
+
+    with row(m) = m, or index[m] // index_div of an int32 `index` [rows] (with
+    src_pair and k: each pair's token).  The groups' sizes stay on the device;
+    rows behind the last group, or with an index outside a, are left as they
+    were (in a new result: undefined).
+
+    a [rows, K] bf16, fp16 or FP8Rows; w [experts, N or 2N, K] of its type, at
+    most 1024 experts, or FP8Rows of codes [experts, N or 2N, K] with scales
+    [experts, N or 2N] or [experts, N or 2N, K/32]; K as for linear.  offsets
+    int32 [experts + 1]; bias [experts, N or 2N] bf16, fp16 or fp32.  Returns
+    [rows, N] of `out_dtype` (a's type by default, bf16 for FP8Rows), or FP8Rows
+    with "mx" scales for "mx" (N a multiple of 32).  `out` receives the result.
+
+    FP8Rows with a 16-bit result may run on the scaled matrix instruction as
+    dense.linear says, where the rows are more than 16 to an expert."""
+    kind, T, K, lda, a_at, av, a_sc, a_sc_at = _operand(a, "a")
+    E, rows, wK, ldw, each, wv, w_sc = _expert_weights(w, kind, "a")
+    if wK != K:
+        raise ValueError(f"w must have {K} columns, as a")
+    if not (gated is False or gated is True):
+        raise ValueError("gated must be True or False")
+    if gated and rows % 2:
+        raise ValueError("a gated w has an even number of rows")
+    N = rows // 2 if gated else rows
+    try:
+        act_id = _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {[k for k in _ACTS]}, not {act!r}") from None
+    offsets_at = _vector(offsets, "offsets", torch.int32, ((E + 1,),))
+    P, index_at = T, None
+    if index is not None:
+        _need(isinstance(index, torch.Tensor) and index.dim() == 1, "index must be an int32 [rows] tensor")
+        P = index.shape[0]
+        index_at = _vector(index, "index", torch.int32, ((P,),))
+    if not (isinstance(index_div, int) and 1 <= index_div <= 0x7FFFFFFF):
+        raise ValueError("index_div must be a positive integer")
+    bias_type, bias_at = 0, None
+    if bias is not None:
+        _need(isinstance(bias, torch.Tensor) and bias.dtype in _FLOATS, "bias must be a bf16, fp16 or fp32 tensor")
+        bias_at, bias_type = _vector(bias, "bias", bias.dtype, ((E, rows),)), _TYPES[bias.dtype]
+    mx = isinstance(out_dtype, str)
+    ldo = N
+    if mx:
+        _need(out_dtype == "mx", 'out_dtype must be bf16, fp16, fp32 or "mx"')
+        if N % 32:
+            raise ValueError(f'an "mx" result needs a multiple of 32 columns, not {N}')
+        _need(out is None, 'out is not taken with out_dtype "mx"')
+        out_type = _lib.TYPE_FP8_MX
+    else:
+        if out_dtype is None:
+            out_dtype = out.dtype if isinstance(out, torch.Tensor) else \
+                torch.bfloat16 if a_sc is not None else av.dtype
+        out_type = _TYPES.get(out_dtype)
+        _need(out_type is not None, 'out_dtype must be bf16, fp16, fp32 or "mx"')
+        if out is not None:
+            ldo = _plain(out, "out", (P, N), (out_dtype,))
+            _check_apart(out, "out", (av, wv, a_sc, w_sc, bias, offsets, index))
+    _lib._check_size(P, "rows of the result")
+    handle, ctx = _on((av, wv, a_sc, w_sc, bias, offsets, index, out), stream)
+    with ctx:
+        out_scales = None
+        if mx:
+            res, out_scales = _fp8_out(P, N, "mx")
+        else:
+            res = _empty(P, N, out_dtype) if out is None else out
+        _lib.grouped_linear(_lib.GroupedLinear(
+            a_at, a_sc_at, wv.data_ptr(), None if w_sc is None else w_sc.data_ptr(), bias_at, offsets_at,
+            index_at, res.data_ptr(), None if out_scales is None else out_scales.data_ptr(), lda, ldw, each,
+            ldo, P, T, E, N, K, index_div, kind, bias_type, out_type, act_id, gated), handle)
+    return FP8Rows(res, out_scales) if mx else res
+
+
 def combine(values: torch.Tensor, weights: torch.Tensor, inv_pair: torch.Tensor, *,
             residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -117,3 +229,46 @@ def combine(values: torch.Tensor, weights: torch.Tensor, inv_pair: torch.Tensor,
         _lib.combine(_TYPES[values.dtype], v_at, ldv, P, w_at, inv_at, T, k, H, r_type, r_at, ldr,
                      _TYPES[out_dtype], out.data_ptr(), ldo, handle)
     return out
+
+
+class ExpertsLayer:
+    """A layer's routed experts held in 16 or 8 bits: what moe.NVFP4MoELayer runs
+    in 4.  w13 [experts, 2 * inter, hidden] (gate rows, then up rows) and w2
+    [experts, hidden, inter]: bf16 or fp16 tensors, or FP8Rows (codes and scales
+    with the experts first) of which `quantized` makes a layer.  act: the gate's
+    activation; bias13 [experts, 2 * inter], bias2 [experts, hidden]."""
+
+    def __init__(self, w13: Operand, w2: Operand, *, act: str = "silu", bias13: Optional[torch.Tensor] = None,
+                 bias2: Optional[torch.Tensor] = None):
+        self.w13, self.w2, self.act, self.bias13, self.bias2 = w13, w2, act, bias13, bias2
+        self.scales = None
+        if isinstance(w13, tuple):
+            self.scales = "row" if w13[1].dtype == torch.float32 else "mx"
+        self.num_experts = (w13 if self.scales is None else w13[0]).shape[0]
+
+    @classmethod
+    def quantized(cls, w13: torch.Tensor, w2: torch.Tensor, scales: str = "mx", **kw) -> "ExpertsLayer":
+        """The layer in 8 bits, from bf16 or fp16 weights."""
+        def fp8(w):
+            q = quantize_fp8(w.reshape(-1, w.shape[2]), scales)
+            return FP8Rows(*(t.view(*w.shape[:2], *t.shape[1:]) for t in q))
+        return cls(fp8(w13), fp8(w2), **kw)
+
+    def forward(self, x: Operand, logits: torch.Tensor, k: int, residual: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+        """x [tokens, hidden] and fp32 logits [tokens, experts] -> [tokens, hidden] of
+        `out_dtype` (x's type by default, bf16 for FP8Rows).  A layer in 8 bits takes x as
+        FP8Rows with its kind of scales, or quantises it.  The experts' rows stay in fp32
+        up to the combine, as in moe."""
+        if out_dtype is None:
+            out_dtype = x.dtype if isinstance(x, torch.Tensor) else torch.bfloat16
+        if self.scales is not None and isinstance(x, torch.Tensor):
+            x = quantize_fp8(x, self.scales, stream=stream)
+        r = route(logits, k, stream=stream)
+        g = permute(r.ids, self.num_experts, stream=stream)
+        h = grouped_linear(x, self.w13, g.offsets, index=g.src_pair, index_div=k, bias=self.bias13, act=self.act,
+                           gated=True, out_dtype="mx" if self.scales == "mx" else None, stream=stream)
+        if self.scales == "row":
+            h = quantize_fp8(h, "row", stream=stream)
+        v = grouped_linear(h, self.w2, g.offsets, bias=self.bias2, out_dtype=torch.float32, stream=stream)
+        return combine(v, r.weights, g.inv_pair, residual=residual, out_dtype=out_dtype, stream=stream)
