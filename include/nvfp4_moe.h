@@ -720,6 +720,34 @@ NVFP4_API nvfp4_status_t nvfp4_linear_workspace_size(const nvfp4_linear_t* p, si
 NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace,
                                       size_t workspace_bytes, nvfp4_stream_t stream);
 
+/* Block scales of 4-bit weights (nvfp4_linear_w4). */
+typedef enum {
+  NVFP4_W4_NV = 0,          /* E4M3, one per 16 elements: uint8 [rows, K/16]            */
+  NVFP4_W4_MX = 1           /* UE8M0, one per 32 elements: uint8 [rows, K/32], 255 NaN  */
+} nvfp4_w4_t;
+
+/*
+ * nvfp4_linear_w4 — nvfp4_linear with weights in 4 bits and activations in 16:
+ *     v[m, n] = gain * sum_k a[m, k] * E2M1(w[n, k]) * scale (+ bias[n]),
+ * the rest as there.  p->type is that of a (NVFP4_TYPE_BF16 or NVFP4_TYPE_FP16); p->w
+ * holds E2M1 codes as everywhere (element 2j in the low nibble of byte j), uint8 [N or
+ * 2N, ldw], ldw in bytes, 16-byte aligned, a multiple of 16, at least K/2; p->w_scales
+ * the block scales, contiguous, NVFP4_W4_NV 2-byte aligned; K % 32 == 0.  Every product is
+ * exact, sums are fp32 sums.  An element code * scale of NVFP4_W4_MX is taken in bf16's
+ * range (infinite from 2^128 on, a multiple of 2^-133 below 2^-126); with fp16
+ * activations a is split into two exact bf16 parts.
+ *
+ *   gain   device fp32 [1] (weight_scale_2) or NULL for 1.
+ * Limits as for nvfp4_linear, with fp16 and NVFP4_W4_MX K <= 2^21; N' * K <= 2^36 and
+ * M * K <= 2^34, N' the rows of w (else NVFP4_ERR_UNSUPPORTED).  The workspace holds w in
+ * 16 bits where M is more than 64.
+ */
+NVFP4_API nvfp4_status_t nvfp4_linear_w4_workspace_size(const nvfp4_linear_t* p, int32_t w4,
+                                                        size_t* bytes);
+NVFP4_API nvfp4_status_t nvfp4_linear_w4(const nvfp4_linear_t* p, int32_t w4, const float* gain,
+                                         void* workspace, size_t workspace_bytes,
+                                         nvfp4_stream_t stream);
+
 /*
  * ---- The routed experts in 16 or 8 bits, step by step --------------------------
  * nvfp4_route_topk and nvfp4_permute above, then the products, then the combine.

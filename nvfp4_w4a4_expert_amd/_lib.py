@@ -106,6 +106,7 @@ _LINEAR_NAMES = tuple(name for name, _ in LinearFields._fields_)
 FP8_NONE = -1
 TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_FP8_ROW, TYPE_FP8_MX = range(5)
 GATE_PLAIN, GATE_SIGMOID, GATE_TANH = range(3)
+W4_NV, W4_MX = range(2)
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
 
 MOE_STAGES = ("route", "permute", "quantize_a1", "gemm1_w13", "gemm2_w2", "combine")
@@ -144,6 +145,8 @@ _SIGS = {
     "nvfp4_quantize_rows_fp8": (_i32, [_i32, _p, _i64, _i32, _i32, _i32, _p, _p, _p]),
     "nvfp4_linear_workspace_size": (_i32, [ctypes.POINTER(LinearFields), ctypes.POINTER(ctypes.c_size_t)]),
     "nvfp4_linear": (_i32, [ctypes.POINTER(LinearFields), _p, ctypes.c_size_t, _p]),
+    "nvfp4_linear_w4_workspace_size": (_i32, [ctypes.POINTER(LinearFields), _i32, ctypes.POINTER(ctypes.c_size_t)]),
+    "nvfp4_linear_w4": (_i32, [ctypes.POINTER(LinearFields), _i32, _p, _p, ctypes.c_size_t, _p]),
     "nvfp4_grouped_linear": (_i32, [ctypes.POINTER(GroupedLinear), _p]),
     "nvfp4_combine": (_i32, [_i32, _p, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _i64, _i32,
                              _p, _i64, _p]),
@@ -387,6 +390,19 @@ def linear(p: LinearFields, workspace, workspace_bytes: int, stream):
     status = _lib.nvfp4_linear(ctypes.byref(p), workspace, workspace_bytes, stream)
     if status != OK:
         raise NVFP4Error(status, "nvfp4_linear")
+
+
+def linear_w4_workspace_size(p: LinearFields, w4: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.nvfp4_linear_w4_workspace_size(ctypes.byref(p), w4, ctypes.byref(n)),
+           "nvfp4_linear_w4_workspace_size")
+    return n.value
+
+
+def linear_w4(p: LinearFields, w4: int, gain, workspace, workspace_bytes: int, stream):
+    status = _lib.nvfp4_linear_w4(ctypes.byref(p), w4, gain, workspace, workspace_bytes, stream)
+    if status != OK:
+        raise NVFP4Error(status, "nvfp4_linear_w4")
 
 
 def grouped_linear(p: GroupedLinear, stream):

@@ -24,7 +24,8 @@ ARCH = "gfx950"
 JOBS = 6                      # compilers at once
 
 SOURCES = ["api.cpp", "quant.hip", "route.hip", "gemm.hip", "combine.hip", "noalloc.hip",
-           "dense.cpp", "rows.hip", "block.hip", "linear.hip", "grouped.hip"]
+           "dense.cpp", "rows.hip", "block.hip", "linear.hip", "linear4.hip",
+           "grouped.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1,6 +1,6 @@
 // C ABI of the dense operators around the routed experts: argument checking of
-// nvfp4_rmsnorm, nvfp4_block_norm, nvfp4_quantize_rows_fp8, nvfp4_linear, nvfp4_grouped_linear
-// and nvfp4_combine.
+// nvfp4_rmsnorm, nvfp4_block_norm, nvfp4_quantize_rows_fp8, nvfp4_linear, nvfp4_linear_w4,
+// nvfp4_grouped_linear and nvfp4_combine.
 #include <math.h>
 #include <stdint.h>
 
@@ -61,6 +61,45 @@ nvfp4_status_t check_linear_sizes(const nvfp4_linear_t* p, LinearArgs* a) {
   a->kind = operand_kind(p->type);
   a->act = p->act; a->gated = p->gated;
   a->out_type = elem_type(p->out_type);
+  return NVFP4_OK;
+}
+
+// The epilogue's tensors of nvfp4_linear and nvfp4_linear_w4.
+nvfp4_status_t check_extra_types(const nvfp4_linear_t* p) {
+  if (p->bias && !is_float_type(p->bias_type)) return NVFP4_ERR_INVALID_ARG;
+  if (p->residual && !is_float_type(p->residual_type)) return NVFP4_ERR_INVALID_ARG;
+  return NVFP4_OK;
+}
+
+nvfp4_status_t check_epilogue(const nvfp4_linear_t* p) {
+  if (p->bias && !aligned(p->bias, float_size(p->bias_type))) return NVFP4_ERR_INVALID_ARG;
+  if (p->residual && (p->ldr < p->N || !aligned(p->residual, float_size(p->residual_type))))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->ldo < p->N) return NVFP4_ERR_INVALID_ARG;
+  if (p->out_type == NVFP4_TYPE_FP8_MX) {
+    if (!p->out_scales || !aligned(p->out, 16) || p->ldo % 16) return NVFP4_ERR_INVALID_ARG;
+  } else if (!aligned(p->out, float_size(p->out_type))) {
+    return NVFP4_ERR_INVALID_ARG;
+  }
+  return NVFP4_OK;
+}
+
+void take_linear(const nvfp4_linear_t* p, LinearArgs* a) {
+  a->a = p->a; a->a_scales = p->a_scales; a->w = p->w; a->w_scales = p->w_scales;
+  a->bias = p->bias; a->residual = p->residual; a->out = p->out; a->out_scales = p->out_scales;
+  a->lda = p->lda; a->ldw = p->ldw; a->ldr = p->ldr; a->ldo = p->ldo;
+  a->bias_type = elem_type(p->bias_type); a->residual_type = elem_type(p->residual_type);
+}
+
+nvfp4_status_t check_w4_sizes(const nvfp4_linear_t* p, int32_t w4, Linear4Args* a) {
+  if (w4 != NVFP4_W4_NV && w4 != NVFP4_W4_MX) return NVFP4_ERR_INVALID_ARG;
+  const nvfp4_status_t st = check_linear_sizes(p, a);
+  if (st != NVFP4_OK) return st;
+  if (is_fp8(p->type) || p->K % 32) return NVFP4_ERR_INVALID_ARG;
+  a->mx = w4 == NVFP4_W4_MX;
+  if (a->mx && p->type == NVFP4_TYPE_FP16 && p->K > (1 << 21)) return NVFP4_ERR_UNSUPPORTED;
+  if ((int64_t)p->N * (p->gated + 1) > ((int64_t)1 << 36) / p->K || p->M > ((int64_t)1 << 34) / p->K)
+    return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_OK;
 }
 
@@ -174,8 +213,8 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, 
   LinearArgs a = {};
   const nvfp4_status_t st = check_linear_sizes(p, &a);
   if (st != NVFP4_OK) return st;
-  if (p->bias && !is_float_type(p->bias_type)) return NVFP4_ERR_INVALID_ARG;
-  if (p->residual && !is_float_type(p->residual_type)) return NVFP4_ERR_INVALID_ARG;
+  const nvfp4_status_t types = check_extra_types(p);
+  if (types != NVFP4_OK) return types;
   if (p->M == 0 || p->N == 0) return NVFP4_OK;
   const bool f8 = is_fp8(p->type);
   const int64_t esz = f8 ? 1 : 2;
@@ -185,22 +224,43 @@ NVFP4_API nvfp4_status_t nvfp4_linear(const nvfp4_linear_t* p, void* workspace, 
   if (f8 && (!p->a_scales || !p->w_scales)) return NVFP4_ERR_INVALID_ARG;
   if (p->type == NVFP4_TYPE_FP8_ROW && (!aligned(p->a_scales, 4) || !aligned(p->w_scales, 4)))
     return NVFP4_ERR_INVALID_ARG;
-  if (p->bias && !aligned(p->bias, float_size(p->bias_type))) return NVFP4_ERR_INVALID_ARG;
-  if (p->residual && (p->ldr < p->N || !aligned(p->residual, float_size(p->residual_type))))
-    return NVFP4_ERR_INVALID_ARG;
-  if (p->ldo < p->N) return NVFP4_ERR_INVALID_ARG;
-  if (p->out_type == NVFP4_TYPE_FP8_MX) {
-    if (!p->out_scales || !aligned(p->out, 16) || p->ldo % 16) return NVFP4_ERR_INVALID_ARG;
-  } else if (!aligned(p->out, float_size(p->out_type))) {
-    return NVFP4_ERR_INVALID_ARG;
-  }
-  a.a = p->a; a.a_scales = p->a_scales; a.w = p->w; a.w_scales = p->w_scales;
-  a.bias = p->bias; a.residual = p->residual; a.out = p->out; a.out_scales = p->out_scales;
-  a.lda = p->lda; a.ldw = p->ldw; a.ldr = p->ldr; a.ldo = p->ldo;
-  a.bias_type = elem_type(p->bias_type); a.residual_type = elem_type(p->residual_type);
+  const nvfp4_status_t rest = check_epilogue(p);
+  if (rest != NVFP4_OK) return rest;
+  take_linear(p, &a);
   const size_t need = linear_workspace_bytes(a);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return NVFP4_ERR_WORKSPACE;
   return device_status(launch_linear(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+NVFP4_API nvfp4_status_t nvfp4_linear_w4_workspace_size(const nvfp4_linear_t* p, int32_t w4, size_t* bytes) {
+  if (!bytes) return NVFP4_ERR_INVALID_ARG;
+  Linear4Args a = {};
+  const nvfp4_status_t st = check_w4_sizes(p, w4, &a);
+  if (st != NVFP4_OK) return st;
+  *bytes = linear4_workspace_bytes(a);
+  return NVFP4_OK;
+}
+
+NVFP4_API nvfp4_status_t nvfp4_linear_w4(const nvfp4_linear_t* p, int32_t w4, const float* gain, void* workspace,
+                                         size_t workspace_bytes, nvfp4_stream_t stream) {
+  Linear4Args a = {};
+  const nvfp4_status_t st = check_w4_sizes(p, w4, &a);
+  if (st != NVFP4_OK) return st;
+  const nvfp4_status_t types = check_extra_types(p);
+  if (types != NVFP4_OK) return types;
+  if (p->M == 0 || p->N == 0) return NVFP4_OK;
+  if (!p->a || !p->w || !p->w_scales || !p->out || !aligned(p->a, 16) || !aligned(p->w, 16) || !aligned(gain, 4) ||
+      !aligned(p->w_scales, a.mx ? 1 : 2))
+    return NVFP4_ERR_INVALID_ARG;
+  if (p->lda < p->K || p->ldw < p->K / 2 || p->lda % 8 || p->ldw % 16) return NVFP4_ERR_INVALID_ARG;
+  if (p->lda * 2 > (1 << 23) || p->ldw > (1 << 23)) return NVFP4_ERR_UNSUPPORTED;
+  const nvfp4_status_t rest = check_epilogue(p);
+  if (rest != NVFP4_OK) return rest;
+  take_linear(p, &a);
+  a.gain = gain;
+  const size_t need = linear4_workspace_bytes(a);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return NVFP4_ERR_WORKSPACE;
+  return device_status(launch_linear4(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 NVFP4_API nvfp4_status_t nvfp4_grouped_linear(const nvfp4_grouped_linear_t* p, nvfp4_stream_t stream) {

@@ -170,8 +170,18 @@ struct LinearArgs {
   int64_t lda, ldw, ldr, ldo;
   int32_t M, N, K;
   int32_t kind, act, gated, bias_type, residual_type, out_type;
+  const float* gain;        // 16-bit operands: multiplies the sums, or null
 };
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream);
+
+// The same with w in 4 bits (linear4.hip): E2M1 codes uint8 [N or 2N, ldw], ldw bytes,
+// w_scales E4M3 [.., K/16] or (mx) UE8M0 [.., K/32], times *gain where given.  kind is
+// a's, 0 or 1.
+struct Linear4Args : LinearArgs {
+  bool mx;
+};
+hipError_t launch_linear4(const Linear4Args& a, void* workspace, hipStream_t stream);
+size_t linear4_workspace_bytes(const Linear4Args& a);  // reads sizes, kind, out_type, gated and mx
 
 // The same product for rows grouped by expert (grouped.hip).
 struct GroupedArgs {

@@ -101,6 +101,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t strea
   p.residual = a.residual;
   p.out = a.out;
   p.out_scales = a.out_scales;
+  p.gain = a.gain;
   p.lda = a.lda * esz;
   p.ldw = a.ldw * esz;
   p.ldr = a.ldr;

@@ -27,6 +27,7 @@ struct LinParams {
   const void* residual;
   void* out;
   uint8_t* out_scales;
+  const float* gain;        // 16-bit kinds: a number that multiplies the sums, or null
   int64_t lda, ldw, ldr, ldo;                                  // lda, ldw in bytes
   int32_t M, N, kbytes;
   int32_t act, bias_type, residual_type, out_type;
@@ -286,6 +287,14 @@ struct Columns {
   __device__ __forceinline__ void finish(const LinParams& p, int64_t m, float* gate, const float* up) const {
     Scale am;
     if constexpr (is_row8(kKind)) am.set(static_cast<const float*>(p.a_scales)[m]);
+    float gain = 1.0f;
+    if constexpr (kKind == kBf16 || kKind == kF16) {
+      if (p.gain) {
+        gain = *p.gain;
+#pragma unroll
+        for (int i = 0; i < kLen; ++i) gate[i] *= gain;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
       if constexpr (is_row8(kKind)) gate[i] = times_scales(gate[i], am, s[i]);
@@ -297,6 +306,7 @@ struct Columns {
       for (int i = 0; i < kLen; ++i) {
         float u = up[i];
         if constexpr (is_row8(kKind)) u = times_scales(u, am, su[i]);
+        else if constexpr (kKind == kBf16 || kKind == kF16) u *= gain;
         gate[i] *= u + bu[i];
       }
     }

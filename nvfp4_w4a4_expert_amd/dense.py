@@ -1,10 +1,11 @@
 """The dense operators around the routed experts, on torch tensors.
 
 ``rms_norm`` adds the residual, normalises and quantises in one pass,
-``block_norm`` does so behind a block's own last norm and gate, ``quantize_fp8`` makes the same 8-bit form of given rows, ``linear`` is a
-matrix product with bias, activation (plain or gated) and residual in its
-epilogue, on bf16, fp16 or 8-bit operands.  A dense feed-forward beside the
-experts, in 8 bits end to end:
+``block_norm`` does so behind a block's own last norm and gate, ``quantize_fp8``
+makes the same 8-bit form of given rows, ``linear`` is a matrix product with
+bias, activation (plain or gated) and residual in its epilogue, on bf16, fp16
+or 8-bit operands, or with weights in 4 bits (``quantize_fp4``).  A dense
+feed-forward beside the experts, in 8 bits end to end:
 
     n = rms_norm(x, weight, residual=h, scales="mx")       # n.y: the experts' bf16 input
     logits = linear(n.y, w_router, out_dtype=torch.float32)
@@ -54,6 +55,26 @@ class FP8Rows(NamedTuple):
             return v * self.scales[:, None]
         s = self.scales.view(torch.float8_e8m0fnu).float()
         return (v.view(*s.shape, 32) * s[..., None]).view(v.shape)
+
+
+class FP4Rows(NamedTuple):
+    """Weights held in 4 bits: E2M1 codes uint8 [rows, K/2] (element 2j in the low
+    nibble of byte j), block scales uint8 [rows, K/16] in E4M3 ("nv") or [rows,
+    K/32] in UE8M0 ("mx"), and an fp32 tensor of one element that multiplies all
+    of them, or None for 1."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+    def dequantize(self) -> torch.Tensor:
+        """The values, in fp32 (with torch operations)."""
+        table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=self.codes.device)
+        c = torch.stack([self.codes & 15, self.codes >> 4], 2).view(self.codes.shape[0], -1).int()
+        v = torch.where(c >= 8, -table[c & 7], table[c & 7])
+        mx = self.codes.shape[1] * 2 == self.scales.shape[1] * 32
+        s = self.scales.view(torch.float8_e8m0fnu if mx else torch.float8_e4m3fn).float()
+        v = (v.view(*s.shape, 32 if mx else 16) * s[..., None]).view(v.shape)
+        return v if self.scale is None else v * self.scale
 
 
 class NormOut(NamedTuple):
@@ -426,13 +447,66 @@ def _plain(t, name, shape, dtypes=_FLOATS):
                      f"{list(shape)} tensor with contiguous rows")
 
 
+def quantize_fp4(w: torch.Tensor, scales: str = "nv", *, stream=None) -> FP4Rows:
+    """bf16 weights [rows, K] -> FP4Rows, at load time: "nv" scales with the fp32
+    scale max|w| / 2688 (1 for a matrix of zeros), or "mx" scales alone.  K is a
+    multiple of 32.  The quantiser is the experts' own (nvfp4_quantize_experts and its
+    UE8M0 form, the matrix as one expert); "nv" waits for the matrix's maximum."""
+    T, K, ldw, _ = _rows(w, "w", None, None, (torch.bfloat16,))
+    if not (isinstance(scales, str) and scales in ("nv", "mx")):
+        raise ValueError('scales must be "nv" or "mx"')
+    _need(K >= 32 and K % 32 == 0, f"w must have a multiple of 32 columns, not {K}")
+    handle, ctx = _on((w,), stream)
+    with ctx:
+        nv = scales == "nv"
+        codes, sf = _empty(T, K // 2, torch.uint8), _empty(T, K // (16 if nv else 32), torch.uint8)
+        ends = torch.tensor([0, T], dtype=torch.int32, device=w.device)
+        scale = gscale = None
+        if nv:
+            scale = _empty_strided((1,), (1,), torch.float32)
+            _lib.expert_absmax(w, ldw, K, None, 1, ends, 1, T, scale, handle)
+            top = scale.item() / 2688.0
+            # (its reciprocal would leave fp32's range below 2^-126)
+            scale.fill_(max(top, 2.0 ** -126) if top > 0 else 1.0)
+            gscale = scale.reciprocal()
+        quant = _lib.quantize_experts if nv else _lib.quantize_experts_mx
+        quant(w, ldw, K, None, T, T, ends, 1, gscale, codes, sf, handle)
+    return FP4Rows(codes, sf, scale)
+
+
+def _fp4_operand(w, K):
+    """(form, rows, row stride in bytes, codes, scales, gain or None) of FP4Rows
+    weights against K columns, checked."""
+    codes, scales, gain = w
+    rows, half, ld, _ = _rows(codes, "w's codes", None, None, _BYTES)
+    if half * 2 != K or K % 32:
+        raise ValueError(f"w must have {K} columns, as a, a multiple of 32" if K % 32 == 0 else
+                         f"a must have a multiple of 32 columns against FP4Rows, not {K}")
+    if not (isinstance(scales, torch.Tensor) and scales.dtype == torch.uint8 and scales.layout is torch.strided and
+            scales.is_contiguous() and scales.shape in ((rows, K // 16), (rows, K // 32))):
+        raise ValueError(f"w's scales must be a contiguous uint8 tensor of shape [{rows}, {K // 16}] or [{rows}, {K // 32}]")
+    mx = scales.shape[1] * 32 == K
+    if not mx and scales.data_ptr() % 2:
+        raise ValueError("w's scales must start on a 2-byte boundary")
+    if gain is not None and not (isinstance(gain, torch.Tensor) and gain.dtype == torch.float32 and gain.numel() == 1 and
+                                 gain.layout is torch.strided):
+        raise ValueError("w's scale must be an fp32 tensor of one element, or None")
+    return _lib.W4_MX if mx else _lib.W4_NV, rows, ld, codes, scales, gain
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes_w4(M, N, K, kind, out_type, gated, w4):
+    return _lib.linear_w4_workspace_size(
+        _lib.Linear(M=M, N=N, K=K, type=kind, out_type=out_type, gated=gated), w4)
+
+
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(M, N, K, kind, out_type, gated):
     return _lib.linear_workspace_size(
         _lib.Linear(M=M, N=N, K=K, type=kind, out_type=out_type, gated=gated))
 
 
-def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
+def linear(a: Operand, w: Union[Operand, FP4Rows], *, bias: Optional[torch.Tensor] = None,
            act: Optional[str] = None, gated: bool = False,
            residual: Optional[torch.Tensor] = None,
            out_dtype: Union[torch.dtype, str, None] = None,
@@ -442,6 +516,9 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
 
     a [M, K] and w [N or 2N, K]: both bf16, both fp16, or both FP8Rows with the
     same kind of scales; K a multiple of 8 (16 for "row", 32 for "mx" operands).
+    Or a in bf16 or fp16 and w as FP4Rows, K a multiple of 32 (nvfp4_linear_w4; all
+    products exact, "mx" weights in bf16's range; for more than 64 rows w is
+    written out in 16 bits, 2 * K bytes a row of memory for the call).
     act: None, "silu", "gelu", "gelu_tanh" or "relu".  bias [N or 2N] and
     residual [M, N]: bf16, fp16 or fp32.  Returns [M, N] of `out_dtype` (a's
     type by default, bf16 for FP8Rows), or FP8Rows with "mx" scales for
@@ -453,11 +530,19 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
     eight neighbours along K; every other form has exact products and fp32 sums.
     So a row may give other bits in a batch of 17 than in one of 16."""
     kind, M, K, lda, a_at, av, a_sc, a_sc_at = _operand(a, "a")
-    wkind, rows, wK, ldw, w_at, wv, w_sc, w_sc_at = _operand(w, "w")
-    if kind != wkind:
-        raise ValueError("a and w must be of one type, with one kind of scales")
-    if wK != K:
-        raise ValueError(f"w must have {K} columns, as a")
+    fp4 = type(w) is FP4Rows
+    gain = None
+    if fp4:
+        if a_sc is not None:
+            raise ValueError("FP4Rows weights take a bf16 or fp16 a")
+        w4, rows, ldw, wv, w_sc, gain = _fp4_operand(w, K)
+        w_at, w_sc_at = wv.data_ptr(), w_sc.data_ptr()
+    else:
+        wkind, rows, wK, ldw, w_at, wv, w_sc, w_sc_at = _operand(w, "w")
+        if kind != wkind:
+            raise ValueError("a and w must be of one type, with one kind of scales")
+        if wK != K:
+            raise ValueError(f"w must have {K} columns, as a")
     if not (gated is False or gated is True):
         raise ValueError("gated must be True or False")
     if gated and rows % 2:
@@ -490,10 +575,11 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
         _need(out_type is not None, 'out_dtype must be bf16, fp16, fp32 or "mx"')
         if out is not None:
             ldo = _plain(out, "out", (M, N), (out_dtype,))
-            _check_apart(out, "out", (av, wv, a_sc, w_sc, bias))
+            _check_apart(out, "out", (av, wv, a_sc, w_sc, bias, gain))
             _check_apart(out, "out", (residual,), True)
-    n = _workspace_bytes(M, N, K, kind, out_type, gated)      # NVFP4Error past the limits, before anything is allocated
-    handle, ctx = _on((av, wv, a_sc, w_sc, bias, residual, out), stream)
+    n = _workspace_bytes_w4(M, N, K, kind, out_type, gated, w4) if fp4 else \
+        _workspace_bytes(M, N, K, kind, out_type, gated)      # NVFP4Error past the limits, before anything is allocated
+    handle, ctx = _on((av, wv, a_sc, w_sc, bias, residual, out, gain), stream)
     with ctx:
         out_scales = None
         if mx:
@@ -506,5 +592,9 @@ def linear(a: Operand, w: Operand, *, bias: Optional[torch.Tensor] = None,
             None if out_scales is None else out_scales.data_ptr(), lda, ldw, ldr, ldo, M, N, K,
             kind, bias_type, res_type, out_type, act_id, gated)
         ws = _empty_strided((n,), (1,), torch.uint8) if n else None
-        _lib.linear(p, None if ws is None else ws.data_ptr(), n, handle)
+        ws_at = None if ws is None else ws.data_ptr()
+        if fp4:
+            _lib.linear_w4(p, w4, None if gain is None else gain.data_ptr(), ws_at, n, handle)
+        else:
+            _lib.linear(p, ws_at, n, handle)
     return FP8Rows(res, out_scales) if mx else res
