@@ -29,11 +29,13 @@ hipError_t go_few(const GroupParams& p, uint32_t blocks, hipStream_t stream) {
 
 template <int kKind, bool kGated>
 hipError_t go(GroupParams p, const GroupPlan& plan, hipStream_t stream) {
-  const uint32_t blocks = (uint32_t)(plan.row_tiles * plan.tiles_n);
+  const uint32_t blocks = (uint32_t)group_blocks(plan.row_tiles, plan.tiles_n);
   p.tiles_n = plan.tiles_n;
   if constexpr (kKind != kRow8 && kKind != kBlock8)
     if (plan.kernel == kFew)
       return p.out_type == kOutBlock8 ? go_few<kKind, 32, kGated>(p, blocks, stream) : go_few<kKind, 16, kGated>(p, blocks, stream);
+  if constexpr (!is_wide(kKind))
+    if (plan.kernel == kTile256) return go_tile<kKind, 256, 2, 4, 2, kGated>(p, blocks, stream);
   if (plan.kernel == kTile128) return go_tile<kKind, 128, 2, 2, 2, kGated>(p, blocks, stream);
   return go_tile<kKind, 64, 2, 2, 4, kGated>(p, blocks, stream);
 }
@@ -52,7 +54,7 @@ GroupPlan plan_for(const GroupedArgs& a) {
 bool grouped_fits(const GroupedArgs& a) {
   if (a.M == 0 || a.N == 0) return true;
   const GroupPlan q = plan_for(a);
-  return q.row_tiles * q.tiles_n <= (q.kernel == kFew ? 0x7FFFFFFF / 512 : 0x7FFFFFFF / 256);
+  return group_blocks(q.row_tiles, q.tiles_n) <= 0x7FFFFFFF / 512;  // threads of a launch, with the kernels' 32-bit numbers
 }
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {

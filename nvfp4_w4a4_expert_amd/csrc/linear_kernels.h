@@ -52,71 +52,93 @@ __device__ __forceinline__ int64_t a_row_of(const LinParams&, int64_t m) { retur
 __device__ __forceinline__ int64_t a_row_of(const GroupParams& p, int64_t m) {
   if (!p.index) return m;
   const int32_t i = p.index[m];
-  if (i < 0) return -1;
   const int32_t r = p.index_div == 1 ? i : (int32_t)((uint32_t)i / (uint32_t)p.index_div);
-  return r < p.a_rows ? r : -1;
+  return i >= 0 && r < p.a_rows ? r : -1;
+}
+
+// Inclusive prefix over a wavefront's lanes of f, whose identity is 0.
+template <class F>
+__device__ __forceinline__ int32_t wave_prefix(int32_t v, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));  // one, two, four and eight lanes up in rows of 16,
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));  // then each row's last lane to the next row
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+  return v;
 }
 
 // What workgroup `block` computes: the tile's expert and place.  Every wavefront finds
-// it by itself, 64 lanes with an equal share of the experts each, from their prefix of
-// row tiles; tiles are numbered expert by expert, within one as tile_at does.
+// it by itself, 64 lanes with an equal share of the experts each, from prefixes over
+// their row tiles.  The groups' last, partly empty tiles are spread evenly among the full
+// ones: the former are bound by reading w, the latter by the matrix units.
 struct GroupTile {
   int32_t expert, first, last;                                 // rows [first, last) of the result; expert -1: nothing to do
   int32_t tm, tn;
 };
 
 __device__ __forceinline__ GroupTile group_tile(const GroupParams& p, int32_t block, int32_t bm) {
+  constexpr int kPer = 1024 / 64;                              // a lane's experts at most
   const int lane = threadIdx.x & 63;
   const int32_t per = (p.experts + 63) / 64, e0 = lane * per;
   // Offsets count as the largest of those up to them, inside the result: out of order or
   // range they leave groups empty, but neither lead out of it nor share rows.
-  auto offset = [&](int32_t e) { return min(max(p.offsets[min(e, p.experts)], 0), p.M); };
-  int32_t most = 0;
-  for (int32_t i = 0; i <= per; ++i) most = max(most, offset(e0 + i));
+  int32_t at[kPer + 1];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int32_t v = __shfl_up(most, d, 64);
-    if (lane >= d) most = max(most, v);
-  }
-  const int32_t before = __shfl_up(most, 1, 64);
-  const int32_t from = max(offset(e0), lane ? before : 0);
-  int32_t sum = 0, lo = from;
-  for (int32_t i = 0; i < per; ++i) {
-    const int32_t hi = max(lo, offset(e0 + i + 1));
-    sum += (hi - lo + bm - 1) / bm;
-    lo = hi;
-  }
-  int32_t upto = sum;
+  for (int i = 0; i <= kPer; ++i)
+    if (i <= per) at[i] = p.offsets[min(e0 + i, p.experts)];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int32_t v = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += v;
-  }
+  for (int i = 0; i <= kPer; ++i)
+    if (i <= per) {
+      at[i] = min(max(at[i], 0), p.M);
+      if (i) at[i] = max(at[i], at[i - 1]);
+    }
+  int32_t last = at[0];
+#pragma unroll
+  for (int i = 1; i <= kPer; ++i)
+    if (i <= per) last = at[i];
+  const int32_t upto_last = wave_prefix(last, [](int32_t a, int32_t b) { return max(a, b); });
+  const int32_t before = __builtin_amdgcn_update_dpp(0, upto_last, 0x138, 0xF, 0xF, false);  // the lane below's
+  int32_t full = 0, rest = 0;
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i)
+    if (i <= per) {
+      at[i] = max(at[i], before);
+      if (i) {
+        full += (at[i] - at[i - 1]) / bm;
+        rest += (at[i] - at[i - 1]) % bm != 0;
+      }
+    }
+  auto add = [](int32_t a, int32_t b) { return a + b; };
+  const int32_t upto_full = wave_prefix(full, add), upto_rest = wave_prefix(rest, add);
+  const int32_t all_full = __builtin_amdgcn_readlane(upto_full, 63), all = all_full + __builtin_amdgcn_readlane(upto_rest, 63);
   GroupTile t;
-  const int32_t total = __builtin_amdgcn_readlane(upto, 63) * p.tiles_n;  // (at most the grid)
   t.expert = -1;
   t.first = t.last = t.tm = t.tn = 0;
-  if (block >= total) return t;
-  const int32_t g = xcd_order(block, total), q = g / p.tiles_n;
-  const int who = (int)__builtin_ctzll(__ballot(upto > q));     // the first prefix beyond q
-  int32_t start = upto - sum, e = e0;
-  lo = from;
-  for (int32_t i = 0; i < per; ++i) {
-    const int32_t hi = max(lo, offset(e0 + i + 1)), tiles = (hi - lo + bm - 1) / bm;
-    if (q < start + tiles || i == per - 1) {
-      e = e0 + i;
-      t.first = lo;
-      t.last = hi;
-      break;
+  int32_t q;
+  group_place(block, all, p.tiles_n, q, t.tn);
+  if (q < 0) return t;
+  const int32_t rest_upto = (int32_t)((int64_t)(q + 1) * (all - all_full) / all);
+  const bool is_full = rest_upto == (int32_t)((int64_t)q * (all - all_full) / all);
+  q = is_full ? q - rest_upto : rest_upto - 1;
+  const int who = (int)__builtin_ctzll(__ballot((is_full ? upto_full : upto_rest) > q));  // the first prefix beyond q
+  int32_t start = is_full ? upto_full - full : upto_rest - rest, e = -1, first = 0, end = 0, tm = 0;
+#pragma unroll
+  for (int i = 1; i <= kPer; ++i)
+    if (i <= per) {
+      const int32_t n = at[i] - at[i - 1], tiles = is_full ? n / bm : (int32_t)(n % bm != 0);
+      if (e < 0 && q < start + tiles) {
+        e = e0 + i - 1;
+        first = at[i - 1];
+        end = at[i];
+        tm = is_full ? q - start : n / bm;
+      }
+      start += tiles;
     }
-    start += tiles;
-    lo = hi;
-  }
   t.expert = __builtin_amdgcn_readlane(e, who);
-  t.first = __builtin_amdgcn_readlane(t.first, who);
-  t.last = __builtin_amdgcn_readlane(t.last, who);
-  start = __builtin_amdgcn_readlane(start, who);
-  tile_at((t.last - t.first + bm - 1) / bm, p.tiles_n, g - start * p.tiles_n, t.tm, t.tn);
+  t.first = __builtin_amdgcn_readlane(first, who);
+  t.last = __builtin_amdgcn_readlane(end, who);
+  t.tm = __builtin_amdgcn_readlane(tm, who);
   return t;
 }
 
@@ -630,7 +652,11 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   constexpr bool kScaled = is_block8(kKind);
   static_assert(kBM + kBN <= 64 * kWaves || !kScaled, "a thread loads the scales of one row");
   static_assert((kStages & (kStages - 1)) == 0, "buffer of a step by masking");
-  __shared__ __align__(1024) char smem[kStages * kStage];
+  // Grouped 256-row tiles: a group's last tile has few rows of a to keep, and w for it
+  // comes from memory, so its steps get as many buffers as LDS holds.
+  constexpr bool kDeep = kGroup && kBM == 256;
+  constexpr int kSmem = kDeep ? 160 * 1024 - (kScaled ? 2 * (kBM + kBN) * 16 : 0) : kStages * kStage;
+  __shared__ __align__(1024) char smem[kSmem];
   __shared__ __align__(16) uint32_t s_scale[kScaled ? 2 : 1][kScaled ? kBM + kBN : 1][4];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -670,14 +696,43 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   int32_t row_at[kGroup ? kLoads : 1];
   if constexpr (kGroup) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      row_at[i] = min(row0 + 8 * i, last_row);
-      if (from.of_a) row_at[i] = (int32_t)max(a_row_of(p, m0 + row_at[i]), (int64_t)0);
+    for (int i = 0; i < kLoads; ++i) row_at[i] = min(row0 + 8 * i, last_row);
+    if (from.of_a) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) row_at[i] += (int32_t)m0;
+      if (p.index) {
+        int32_t pair[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) pair[i] = p.index[row_at[i]];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const uint32_t r = p.index_div == 1 ? (uint32_t)pair[i] : (uint32_t)pair[i] / (uint32_t)p.index_div;
+          row_at[i] = pair[i] >= 0 && r < (uint32_t)p.a_rows ? (int32_t)r : 0;
+        }
+      }
     }
   }
   const int tail = last_bytes(p.kbytes, step0, steps);
-  auto fetch = [&](int ks) {
-    char* dst = smem + (ks & (kStages - 1)) * kStage + wave * kLoads * 1024;
+  int ring = kStages, stage = kStage, a_bytes = kBM * kStep;
+  if constexpr (kDeep) {
+    const int rows = last_row_of(kBM, p.M, m0) + 1;
+    if (rows <= kBM / 2) {
+      a_bytes = (rows <= kBM / 4 ? kBM / 4 : kBM / 2) * kStep;
+      stage = a_bytes + kBN * kStep;
+      ring = rows <= kBM / 4 && !kScaled ? 4 : 3;
+    }
+  }
+  // (a wavefront copies all rows of its part or, behind the last row, none: step_barrier
+  // counts copies)
+  const int my_part = wave * kLoads * 1024 - (from.of_a ? 0 : kBM * kStep - a_bytes);
+  const bool mine = !kDeep || !from.of_a || __builtin_amdgcn_readfirstlane(row0) <= last_row;
+  // step ks's copies, into the buffer at `at`
+  auto fetch = [&](int ks, int at) {
+    if (!mine) {
+      base += kStep;
+      return;
+    }
+    char* dst = smem + at + my_part;
     if (chunk * 16 < (ks == steps - 1 ? tail : kStep)) {
       const uint32_t to = lds_address(dst);
       asm volatile("" : "+v"(row0));                           // (formed here, not carried along)
@@ -693,6 +748,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     base += kStep;
   };
 
+  int slot = 0, slot_next = stage;                              // (kDeep) this step's buffer and the next one's
   f32x4 acc[kFN][kFM];
 #pragma unroll
   for (int j = 0; j < kFN; ++j)
@@ -714,6 +770,24 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
                   ((int64_t)min(n0 + q % kOutN, p.N - 1) + (q >= kOutN ? p.N : 0)) * nblk;
     }
   }
+
+  // Rows of the operands' tiles that a wavefront multiplies: fragment i of a from row
+  // a_first + a_row(i) on, fragment j of w from w_first + w_row(j) on.  Grouped: the
+  // wavefronts' fragments take turns, gate before up, so that a tile whose rows or columns
+  // end early leaves every wavefront the same fewer of them.
+  const int a_first = kGroup ? wm * 16 : wm * kTM, w_first = kGroup ? wn * 16 : wn * kTN;
+  auto a_row = [](int i) { return kGroup ? i * 16 * kWM : i * 16; };
+  auto w_row = [](int j) {
+    if (!kGroup) return j * 16;
+    return kGated ? (j & 1) * kOutN + (j >> 1) * 16 * kWN : j * 16 * kWN;
+  };
+  // Grouped: groups end inside tiles, and empty fragments would cost as much as full ones,
+  // so each wavefront leaves out those of a past the tile's last row, and the second half
+  // of w's where the tile's columns end before.
+  constexpr bool kCut = kGroup && !is_wide(kKind);
+  const int have_i = kCut ? (last_row_of(kBM, p.M, m0) + 16 * kWM) / (16 * kWM) : kFM;
+  constexpr bool kCutColumns = kCut && kFN >= (kGated ? 4 : 2);  // (gate and up stay together)
+  const bool all_j = !kCutColumns || p.N - n0 > kOutN / 2;
 
   // Main loop.  A step runs its groups of instructions (one 16-row fragment of a
   // with all of w) in order, the fragments of a being read kAhead groups ahead; the
@@ -742,9 +816,9 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     for (int c = 0; c < kWords; ++c) {
       const int word = kKind == kBlock8Wide ? 2 * c + g / 2 : g;
 #pragma unroll
-      for (int i = 0; i < kFM; ++i) va[i][c] = s_scale[kScaled ? buf : 0][kScaled ? wm * kTM + i * 16 + i16 : 0][word];
+      for (int i = 0; i < kFM; ++i) va[i][c] = s_scale[kScaled ? buf : 0][kScaled ? a_first + a_row(i) + i16 : 0][word];
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) vw[j][c] = s_scale[kScaled ? buf : 0][kScaled ? kBM + wn * kTN + j * 16 + i16 : 0][word];
+      for (int j = 0; j < kFN; ++j) vw[j][c] = s_scale[kScaled ? buf : 0][kScaled ? kBM + w_first + w_row(j) + i16 : 0][word];
     }
   };
   // The compiler would move the reads back to their uses and the matrix
@@ -761,29 +835,37 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     constexpr int kBase = kFM == 2 ? 2 * (T & 1) : 0;          // slot of group 0
     constexpr int kNext = kFM == 2 ? 2 - 2 * (T & 1) : 0;      // slot of the next step's group 0
     typedef Prepared<kKind, T> Op;
-    const char* ta = smem + (ks & (kStages - 1)) * kStage + wm * kTM * kStep;
-    const char* na = smem + ((ks + 1) & (kStages - 1)) * kStage + wm * kTM * kStep;
-    const char* nw = smem + ((ks + 1) & (kStages - 1)) * kStage + (kBM + wn * kTN) * kStep;
+    const int here = kDeep ? slot : (ks & (kStages - 1)) * kStage;
+    const int next = kDeep ? slot_next : ((ks + 1) & (kStages - 1)) * kStage;
+    const char* ta = smem + here + a_first * kStep;
+    const char* na = smem + next + a_first * kStep;
+    const char* nw = smem + next + a_bytes + w_first * kStep;
     if constexpr (kScaled && T == 0) read_scales((ks >> 2) & 1);
     Op pw[kFN];
 #pragma unroll
     for (int j = 0; j < kFN; ++j) pw[j].set(fw[j], vw[j]);
 #pragma unroll
     for (int i = 0; i < kFM - kAhead; ++i) {
-      fa[(kBase + i + kAhead) & 3] = read_frag(ta, (i + kAhead) * 16 + i16, g);
+      fa[(kBase + i + kAhead) & 3] = read_frag(ta, a_row(i + kAhead) + i16, g);
       hold();
-      Op pa;
-      pa.set(fa[(kBase + i) & 3], va[i]);
-      // the wavefront that has its fragments goes first: 8192^3 with block scales
-      // 501 -> 462 us, nothing lost elsewhere
-      __builtin_amdgcn_s_setprio(1);
+      if (!kCut || i < have_i) {
+        Op pa;
+        pa.set(fa[(kBase + i) & 3], va[i]);
+        // the wavefront that has its fragments goes first: 8192^3 with block scales
+        // 501 -> 462 us, nothing lost elsewhere
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int u = 0; u < kSubs<kKind>; ++u)
+        for (int u = 0; u < kSubs<kKind>; ++u)
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) acc[j][i] = mma<kKind, T>(pw[j], pa, u, acc[j][i]);
+          for (int h = 0; h < 2; ++h)
+            if (h == 0 || !kCutColumns || all_j) {
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) issued(acc[j][i]);
-      __builtin_amdgcn_s_setprio(0);
+              for (int j = h * kFN / 2; j < (h + 1) * kFN / 2; ++j) acc[j][i] = mma<kKind, T>(pw[j], pa, u, acc[j][i]);
+            }
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) issued(acc[j][i]);
+        __builtin_amdgcn_s_setprio(0);
+      }
       hold();
     }
     if constexpr (kScaled) {
@@ -796,26 +878,34 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     // behind the barrier this buffer is read and the next one filled; copies that
     // are on their way then are those of the steps from ks + 2 on
     if (kStages > 2 && ks + kStages <= steps) step_barrier<(kStages - 2) * kLoads>();
+    else if (kDeep && ring == 4 && ks + 4 <= steps) step_barrier<2 * kLoads>();
+    else if (kDeep && ring == 3 && ks + 3 <= steps) step_barrier<kLoads>();
     else step_barrier<0>();
-    if (!kLate && ks + kStages < steps) fetch(ks + kStages);
+    if (!kLate && ks + ring < steps) fetch(ks + ring, here);
     Op pa[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) pa[i].set(fa[(kBase + kFM - kAhead + i) & 3], va[kFM - kAhead + i]);
     // (after the last step these read an older one, unused)
     fa[kNext] = read_frag(na, i16, g);
-    if (kAhead == 2) fa[kNext + 1] = read_frag(na, 16 + i16, g);
+    if (kAhead == 2) fa[kNext + 1] = read_frag(na, a_row(1) + i16, g);
     hold();
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
+      if (!kCut || (kFM - kAhead < have_i && (j < kFN / 2 || !kCutColumns || all_j))) {
 #pragma unroll
-      for (int u = 0; u < kSubs<kKind>; ++u)
+        for (int u = 0; u < kSubs<kKind>; ++u)
 #pragma unroll
-        for (int i = kFM - kAhead; i < kFM; ++i) acc[j][i] = mma<kKind, T>(pw[j], pa[i - kFM + kAhead], u, acc[j][i]);
+          for (int i = kFM - kAhead; i < kFM; ++i) acc[j][i] = mma<kKind, T>(pw[j], pa[i - kFM + kAhead], u, acc[j][i]);
 #pragma unroll
-      for (int i = kFM - kAhead; i < kFM; ++i) issued(acc[j][i]);
-      fw[j] = read_frag(nw, j * 16 + i16, g);
+        for (int i = kFM - kAhead; i < kFM; ++i) issued(acc[j][i]);
+      }
+      fw[j] = read_frag(nw, w_row(j) + i16, g);
       hold();
-      if (kLate && j == 0 && ks + kStages < steps) fetch(ks + kStages);
+      if (kLate && j == 0 && ks + ring < steps) fetch(ks + ring, here);
+    }
+    if constexpr (kDeep) {
+      slot = slot_next;
+      slot_next = slot_next + stage == ring * stage ? 0 : slot_next + stage;
     }
   };
   // The wide kinds' step where a wavefront has four groups: the conversions of each
@@ -841,12 +931,12 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   };
   auto wide_step = [&](auto t, int ks) {
     constexpr int T = decltype(t)::value, N = (T + 1) % 4;
-    const char* ta = smem + (ks & (kStages - 1)) * kStage + wm * kTM * kStep;
-    const char* na = smem + ((ks + 1) & (kStages - 1)) * kStage + wm * kTM * kStep;
-    const char* nw = smem + ((ks + 1) & (kStages - 1)) * kStage + (kBM + wn * kTN) * kStep;
+    const char* ta = smem + (ks & (kStages - 1)) * kStage + a_first * kStep;
+    const char* na = smem + ((ks + 1) & (kStages - 1)) * kStage + a_first * kStep;
+    const char* nw = smem + ((ks + 1) & (kStages - 1)) * kStage + (kBM + w_first) * kStep;
     WideOp wb[2];
-    fa[2] = read_frag(ta, 32 + i16, g);
-    fa[3] = read_frag(ta, 48 + i16, g);
+    fa[2] = read_frag(ta, a_row(2) + i16, g);
+    fa[3] = read_frag(ta, a_row(3) + i16, g);
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
       if (j == 0) ww[kFN - 1].template widen<T>(fw[kFN - 1], vw[kFN - 1]);
@@ -863,25 +953,25 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     step_barrier<0>();
     if constexpr (kScaled && T == 3) read_scales(((ks >> 2) + 1) & 1);
     fa[0] = read_frag(na, i16, g);
-    fa[1] = read_frag(na, 16 + i16, g);
+    fa[1] = read_frag(na, a_row(1) + i16, g);
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
       if (j > 0) ww[j - 1].template widen<N>(fw[j - 1], vw[j - 1]);
       if (j >= 2) wa[j - 2].template widen<N>(fa[j - 2], va[j - 2]);
       pair(j, 2, wb);
-      fw[j] = read_frag(nw, j * 16 + i16, g);
+      fw[j] = read_frag(nw, w_row(j) + i16, g);
       mix(std::integral_constant<int, 3>{});
-      if (j == 0 && ks + kStages < steps) fetch(ks + kStages);
+      if (j == 0 && ks + kStages < steps) fetch(ks + kStages, (ks & (kStages - 1)) * kStage);
     }
   };
-  for (int ks = 0; ks < kStages && ks < steps; ++ks) fetch(ks);
+  for (int ks = 0; ks < ring && ks < steps; ++ks) fetch(ks, ks * stage);
   if constexpr (kScaled)
     if (threadIdx.x < kBM + kBN) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = scale_words(load_scales(scale_row, 4 * step0, nblk));
   step_barrier<0>();
 #pragma unroll
-  for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + (kBM + wn * kTN) * kStep, j * 16 + i16, g);
-  fa[0] = read_frag(smem + wm * kTM * kStep, i16, g);
-  if (kAhead == 2) fa[1] = read_frag(smem + wm * kTM * kStep, 16 + i16, g);
+  for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + a_bytes + w_first * kStep, w_row(j) + i16, g);
+  fa[0] = read_frag(smem + a_first * kStep, i16, g);
+  if (kAhead == 2) fa[1] = read_frag(smem + a_first * kStep, a_row(1) + i16, g);
   if constexpr (kWideStep) {
     if constexpr (kScaled) read_scales(0);
 #pragma unroll
@@ -913,34 +1003,39 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   constexpr int kRowsPerIter = 64 * kWaves / kPer, kIters = kRows / kRowsPerIter;
   static_assert(kRows * kLd * 4 <= kStages * kStage && kRows % kRowsPerIter == 0, "the pass fits the step buffers");
   float* tile = reinterpret_cast<float*>(smem);
+  // the tile's row behind row r of a pass (wavefront row, fragment, row)
+  auto tile_row = [&](int r, int pass) {
+    if (!kGroup) return (r / 32) * kTM + pass * 32 + r % 32;
+    return r / 32 * 16 + a_row(2 * pass + (r / 16 & 1)) + (r & 15);
+  };
   const int c = (int)(threadIdx.x % kPer) * 8;
   const int32_t n = n0 + c;
   Columns<kKind, kGated, 8> cols;
   cols.load(p, n);
 #pragma unroll 1
-  for (int pass = 0; pass < kFM / 2; ++pass) {
+  for (int pass = 0; pass < (kCut ? (have_i + 1) / 2 : kFM / 2); ++pass) {
     Residual<8> res[kIters];
 #pragma unroll
     for (int k = 0; k < kIters; ++k) {
       const int r = (int)threadIdx.x / kPer + k * kRowsPerIter;
       if constexpr (!kGroup)
-        if (whole) res[k].load(p, min(m0 + (r / 32) * kTM + pass * 32 + r % 32, (int64_t)p.M - 1), n);
+        if (whole) res[k].load(p, min(m0 + tile_row(r, pass), (int64_t)p.M - 1), n);
     }
     lds_barrier();                                             // the steps' (or the last pass's) reads are done
-    float* dst = tile + (wm * 32 + i16) * kLd + wn * kTN + 4 * g;
+    float* dst = tile + (wm * 32 + i16) * kLd + w_first + 4 * g;
 #pragma unroll
     for (int q = 0; q < kFM / 2; ++q)
       if (q == pass) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < kFN; ++j) *reinterpret_cast<f32x4*>(dst + i * 16 * kLd + j * 16) = acc[j][2 * q + i];
+          for (int j = 0; j < kFN; ++j) *reinterpret_cast<f32x4*>(dst + i * 16 * kLd + w_row(j)) = acc[j][2 * q + i];
       }
     lds_barrier();
 #pragma unroll
     for (int k = 0; k < kIters; ++k) {
       const int r = (int)threadIdx.x / kPer + k * kRowsPerIter;
-      const int64_t m = m0 + (r / 32) * kTM + pass * 32 + r % 32;
+      const int64_t m = m0 + tile_row(r, pass);
       const int64_t ma = a_row_of(p, m < p.M ? m : (int64_t)p.M - 1);
       const bool in = m < p.M && n < p.N && ma >= 0;
       const int64_t mr = max(ma, (int64_t)0);

@@ -98,6 +98,15 @@ inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) 
   return best;
 }
 
+// 8-bit operands: the exact instructions where fp32's accuracy shows in the output
+// (fp32 itself; block scales, which change by a factor of two at a border) and where
+// reading w is the bound anyway.
+inline int kind_of(int kind, int32_t M, int32_t out_type) {
+  if (kind != kRow8 && kind != kBlock8) return kind;
+  if (M > 16 && out_type != kOutF32 && out_type != kOutBlock8) return kind;
+  return kind == kRow8 ? kRow8Wide : kBlock8Wide;
+}
+
 // The kernel of a product grouped by expert: M rows over `experts` groups of sizes that
 // only the device knows.  row_tiles is the most tiles (of 16 rows for the few-row form)
 // that M rows can fall into; tiles beyond those in use end at once.
@@ -110,21 +119,12 @@ struct GroupPlan {
 inline GroupPlan group_plan_of(int32_t M, int32_t experts, int32_t N, int32_t kbytes, int kind, bool gated, int out_type) {
   const int32_t groups = M < experts ? M : experts, mean = M / groups;
   GroupPlan q;
-  q.kernel = mean <= 16 ? kFew : mean <= 96 ? kTile64 : kTile128;
-  q.tile = q.kernel == kFew ? 16 : q.kernel == kTile64 ? 64 : 128;
+  q.kernel = mean <= 16 ? kFew : mean <= 96 ? kTile64 : is_wide(kind_of(kind, 17, out_type)) ? kTile128 : kTile256;
+  q.tile = q.kernel == kFew ? 16 : q.kernel == kTile64 ? 64 : q.kernel == kTile128 ? 128 : 256;
   const int32_t columns = q.kernel == kFew ? (out_type == kOutBlock8 ? 32 : 16) : gated ? q.tile / 2 : q.tile;
   q.tiles_n = (N - 1) / columns + 1;
   q.row_tiles = (int64_t)(M - groups) / q.tile + groups;
   return q;
-}
-
-// 8-bit operands: the exact instructions where fp32's accuracy shows in the output
-// (fp32 itself; block scales, which change by a factor of two at a border) and where
-// reading w is the bound anyway.
-inline int kind_of(int kind, int32_t M, int32_t out_type) {
-  if (kind != kRow8 && kind != kBlock8) return kind;
-  if (M > 16 && out_type != kOutF32 && out_type != kOutBlock8) return kind;
-  return kind == kRow8 ? kRow8Wide : kBlock8Wide;
 }
 
 // The g-th of `total` workgroups in an order that gives each of the 8 XCDs (which
@@ -133,6 +133,27 @@ NVFP4_LINEAR_HD int32_t xcd_order(int32_t g, int32_t total) {
   const int32_t per = total / 8, rest = total % 8, xcd = g % 8;
   return xcd * per + (xcd < rest ? xcd : rest) + g / 8;
 }
+
+// Place of workgroup `block` of a grouped product of row_tiles x tiles_n tiles: the tile
+// row among all groups' and the column, row -1 where there is none.  Tiles differ in
+// cost (a group's last one has few rows), so whole tile rows go to the XCDs in turn; of
+// those that are left in the end each XCD gets an equal run of tiles.
+NVFP4_LINEAR_HD void group_place(int32_t block, int32_t row_tiles, int32_t tiles_n, int32_t& row, int32_t& column) {
+  const int32_t turns = row_tiles / 8, left = (row_tiles - 8 * turns) * tiles_n;
+  const int32_t xcd = block % 8, i = block / 8;
+  if (i < turns * tiles_n) {
+    row = i / tiles_n * 8 + xcd;
+    column = i % tiles_n;
+    return;
+  }
+  const int32_t at = (i - turns * tiles_n) * 8 + xcd;
+  const int32_t g = at < left ? xcd_order(at, left) : 0;
+  row = at < left ? 8 * turns + g / tiles_n : -1;
+  column = g % tiles_n;
+}
+
+// Workgroups that hold every place of at most row_tiles tile rows.
+NVFP4_LINEAR_HD int64_t group_blocks(int64_t row_tiles, int32_t tiles_n) { return (row_tiles * tiles_n + 7) / 8 * 8; }
 
 // Tile number -> (tile row, tile column): bands of 8 tile rows, each walked down
 // its columns, so that neighbours share rows of a and of w in their L2.

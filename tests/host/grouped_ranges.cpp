@@ -27,29 +27,30 @@ static void walk(const std::vector<int32_t>& sizes, int32_t N, bool gated, int k
   for (int32_t s : sizes) M += s;
   if (M == 0) return;
   const GroupPlan q = group_plan_of((int32_t)M, (int32_t)sizes.size(), N, 2816 * 2, kind, gated, out_type);
-  int64_t used = 0;
-  std::vector<int64_t> start;
-  for (int32_t s : sizes) {
-    start.push_back(used);
-    used += (s + q.tile - 1) / q.tile;
-  }
+  // tile rows: full ones of every group, then the groups' last ones
+  std::vector<std::pair<int32_t, int32_t>> rows;
+  for (size_t e = 0; e < sizes.size(); ++e)
+    for (int32_t t = 0; t < sizes[e] / q.tile; ++t) rows.push_back({(int32_t)e, t});
+  for (size_t e = 0; e < sizes.size(); ++e)
+    if (sizes[e] % q.tile) rows.push_back({(int32_t)e, sizes[e] / q.tile});
+  const int64_t used = (int64_t)rows.size(), total = used * q.tiles_n;
   need(used <= q.row_tiles, "the grid holds all row tiles", used, q.row_tiles);
-  const int64_t total = used * q.tiles_n;
-  need(q.row_tiles * q.tiles_n <= 0x7FFFFFFF, "32-bit numbers", total);
+  const int64_t blocks = group_blocks(q.row_tiles, q.tiles_n);
+  need(blocks <= 0x7FFFFFFF && blocks >= total, "32-bit numbers", blocks);
   std::vector<char> seen(total, 0);
-  for (int64_t block = 0; block < total; ++block) {
-    const int32_t g = xcd_order((int32_t)block, (int32_t)total), at = g / q.tiles_n;
-    size_t e = 0;
-    while (start[e] + (sizes[e] + q.tile - 1) / q.tile <= at) ++e;
-    need(e < sizes.size() && sizes[e] > 0, "a group with rows", e);
-    const int32_t tiles = (sizes[e] + q.tile - 1) / q.tile;
-    int32_t tm, tn;
-    tile_at(tiles, q.tiles_n, (int32_t)(g - start[e] * q.tiles_n), tm, tn);
-    need(tm >= 0 && tm < tiles && tn >= 0 && tn < q.tiles_n, "tile of the group", tm, tn);
-    const int64_t id = (start[e] + tm) * q.tiles_n + tn;
+  std::vector<int64_t> per_xcd(8, 0);
+  for (int64_t block = 0; block < blocks; ++block) {
+    int32_t row, column;
+    group_place((int32_t)block, (int32_t)used, q.tiles_n, row, column);
+    if (row < 0) continue;
+    need(row < used && column >= 0 && column < q.tiles_n, "a place", row, column);
+    const int64_t id = (int64_t)row * q.tiles_n + column;
     need(!seen[id], "each tile once", id);
     seen[id] = 1;
+    ++per_xcd[block % 8];
   }
+  const auto range = std::minmax_element(per_xcd.begin(), per_xcd.end());
+  need(*range.second - *range.first <= 1, "XCDs get equal numbers", *range.first, *range.second);
   for (char c : seen) need(c, "every tile");
 }
 
