@@ -26,46 +26,32 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-// A lane's block scales of 32 elements: E4M3 codes in bytes 0 and 1, or a UE8M0 code in
-// byte 0.  Element runs of 8 (t) as 16-bit numbers.
-template <bool kMx, bool kHalf>
-struct Scale4;
-template <>
-struct Scale4<false, false> {
-  f32x2_t s;
-  __device__ __forceinline__ void set(uint32_t c) { s = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false); }
-  __device__ __forceinline__ u32x4 weights(uint32_t w, int t) const {
-    const float v = t < 2 ? s.x : s.y;
-    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    // (the products are bf16 numbers: their upper halves)
-    auto pair = [&](const f32x2_t& x) { return __builtin_amdgcn_perm(__float_as_uint(x.y * v), __float_as_uint(x.x * v), 0x07060302u); };
-    return u32x4{pair(a), pair(b), pair(c), pair(d)};
-  }
-};
-template <>
-struct Scale4<false, true> {
-  half2_t s;
-  __device__ __forceinline__ void set(uint32_t c) { s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false); }
-  __device__ __forceinline__ u32x4 weights(uint32_t w, int t) const {
-    const half2_t v = t < 2 ? half2_t{s.x, s.x} : half2_t{s.y, s.y};
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * v),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * v),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * v),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * v)};
-  }
-};
-template <bool kHalf>
-struct Scale4<true, kHalf> {                                    // (bf16 weights for either a)
-  float s;
-  __device__ __forceinline__ void set(uint32_t c) { s = __uint_as_float((c & 0xFFu) << 23); }
-  __device__ __forceinline__ u32x4 weights(uint32_t w, int) const {
+// Eight elements as 16-bit numbers: a word of codes times the block scale in byte kByte
+// of `scales`.
+template <bool kMx, bool kHalf, int kByte>
+__device__ __forceinline__ u32x4 weights8(uint32_t w, uint32_t scales) {
+  if constexpr (kMx) {                                         // (bf16 for either a)
+    const float s = __uint_as_float(((scales >> (8 * kByte)) & 0xFFu) << 23);
     return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+  } else if constexpr (kHalf) {
+    const half2_t v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales, 1.0f, kByte >= 2);
+    const half2_t s = kByte % 2 ? half2_t{v.y, v.y} : half2_t{v.x, v.x};
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s)};
+  } else {
+    const float s = __builtin_amdgcn_cvt_f32_fp8((int)scales, kByte);
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+    const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    // (the products are bf16 numbers: their upper halves)
+    auto pair = [&](const f32x2_t& x) { return __builtin_amdgcn_perm(__float_as_uint(x.y * s), __float_as_uint(x.x * s), 0x07060302u); };
+    return u32x4{pair(a), pair(b), pair(c), pair(d)};
   }
-};
+}
 
 // 8 fp16 numbers as bf16 numbers hi + lo: the upper 8 significant bits and the rest.
 __device__ __forceinline__ void split_f16(const u32x4& a, u32x4& hi, u32x4& lo) {
@@ -97,10 +83,39 @@ __device__ __forceinline__ f32x4 mma4(const u32x4& w, const u32x4& a, f32x4 acc)
 // ---- few rows -------------------------------------------------------------------
 // A workgroup owns 16 * kFN rows of w (gated: gate rows, then up rows) and 16 * kRF rows
 // of a.  Its wavefronts take groups of 128 elements of K in turn, kBatch groups' loads in
-// flight at once: a lane's 16 bytes of w are 32 elements of a row, the next 32 belong to
-// the next group of 16 lanes, and the four matrix instructions of a group take 8
-// elements of each (any order of K that both operands share).  The wavefronts' sums are
-// added in order through LDS, 16 rows at a time.
+// flight at once.  The t-th of a group's four matrix instructions takes elements 32 t ..
+// 32 t + 31, lane group g eight from 8 g on: a's loads are then 64 bytes of a row in one
+// piece.  w comes 16 bytes a lane, 32 elements, and four lane groups exchange words, so
+// that each has its run of all four.  The wavefronts' sums are added in order through
+// LDS, 16 rows at a time.
+//
+// The block scales of 128 elements of a row, `blocks` of them inside it (a multiple of 32
+// elements): 8 bytes of E4M3 at an even address, or 4 of UE8M0 at any.  Those past the
+// end are zeros.
+template <bool kMx>
+__device__ __forceinline__ void load_scales4(const uint8_t* at, int32_t blocks, uint32_t* s) {
+  constexpr int kWords = kMx ? 1 : 2;
+  if (blocks >= 4 * kWords) {
+    __builtin_memcpy(s, at, 4 * kWords);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) s[i] = 0;
+#pragma unroll
+  for (int i = 0; i < 4 * kWords; ++i)
+    if (i < blocks) s[i / 4] |= (uint32_t)at[i] << (8 * (i % 4));
+}
+
+// Word g of the 16 bytes that lane group t loaded, in d[t] of lane group g: a transpose
+// of four words across the four groups of 16 lanes.
+__device__ __forceinline__ u32x4 exchange(const u32x4& w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);   // upper half of one, lower half of the other
+  const auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);  // odd groups of one, even ones of the other
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
 __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
   constexpr int kWaves = 8, kRows = 16 * kFN, kCols = kGated ? kRows / 2 : kRows;
@@ -138,40 +153,43 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
   const int groups = (K + 127) / 128;
   for (int first = kBatch * wave; first < groups; first += kBatch * kWaves) {
     u32x4 w[kBatch][kFN], a[kBatch][kRF][4];
-    uint32_t s[kBatch][kFN];
+    uint32_t s[kBatch][kFN][kMx ? 1 : 2];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       // past the end of a row codes, scales and a count as zeros
-      const int32_t k = (first + b) * 128 + 32 * g;
-      const bool in = k < K;
+      const int32_t k0 = (first + b) * 128;
+      const int32_t blocks = (K - k0) / kBlock;                // (0 or less: none)
 #pragma unroll
       for (int j = 0; j < kFN; ++j) {
         w[b][j] = u32x4{0, 0, 0, 0};
-        s[b][j] = 0;
-        if (in) {
-          w[b][j] = *reinterpret_cast<const u32x4*>(pw[j] + k / 2);
-          if constexpr (kMx) s[b][j] = sw[j][k / 32];
-          else s[b][j] = *reinterpret_cast<const uint16_t*>(sw[j] + k / 16);
-        }
+        if (k0 + 32 * g < K) w[b][j] = *reinterpret_cast<const u32x4*>(pw[j] + k0 / 2 + 16 * g);
+        load_scales4<kMx>(sw[j] + k0 / kBlock, blocks, s[b][j]);
       }
 #pragma unroll
       for (int i = 0; i < kRF; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           a[b][i][t] = u32x4{0, 0, 0, 0};
-          if (in) a[b][i][t] = *reinterpret_cast<const u32x4*>(pa[i] + 2 * k + 16 * t);
+          if (k0 + 32 * t < K) a[b][i][t] = *reinterpret_cast<const u32x4*>(pa[i] + 2 * (k0 + 32 * t + 8 * g));
         }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      Scale4<kMx, kHalf> sc[kFN];
+      u32x4 c[kFN];
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) sc[j].set(s[b][j]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int j = 0; j < kFN; ++j) {
+        c[j] = exchange(w[b][j]);
+        // E4M3: lane groups 0 and 1 take the even blocks, 2 and 3 the odd ones
+        if constexpr (!kMx) {
+          s[b][j][0] >>= 8 * (g >> 1);
+          s[b][j][1] >>= 8 * (g >> 1);
+        }
+      }
+      auto part = [&](auto tc) {
+        constexpr int t = decltype(tc)::value;
         u32x4 wt[kFN];
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) wt[j] = sc[j].weights(w[b][j][t], t);
+        for (int j = 0; j < kFN; ++j) wt[j] = weights8<kMx, kHalf, kMx ? t : t % 2 * 2>(c[j][t], s[b][j][kMx ? 0 : t / 2]);
 #pragma unroll
         for (int i = 0; i < kRF; ++i) {
           if constexpr (kSplit) {
@@ -186,7 +204,11 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
             for (int j = 0; j < kFN; ++j) acc[i][j] = mma4<kMx, kHalf>(wt[j], a[b][i][t], acc[i][j]);
           }
         }
-      }
+      };
+      part(std::integral_constant<int, 0>{});
+      part(std::integral_constant<int, 1>{});
+      part(std::integral_constant<int, 2>{});
+      part(std::integral_constant<int, 3>{});
     }
   }
 
@@ -228,6 +250,203 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
   }
 }
 
+// ---- middle numbers of rows -----------------------------------------------------------
+// A workgroup of four wavefronts owns kBM = 16 kFM rows of a and 128 rows of w (gated: 64
+// gate rows and their up rows), each wavefront 32 of the latter, and all or a part of
+// K.  Reading w once would cost less than reading a again for every few rows of w (M = 64,
+// 8192 x 8192: 268 MB from L2 in the form above), so both go to LDS, 128 elements of K a
+// step and w as codes; a wavefront widens its own rows of w, once for all rows of a.  Lane
+// group g holds elements 32 g .. 32 g + 31 of a step, the t-th matrix instruction takes
+// eight of them.
+constexpr int kRowsW = 128;                                    // rows of w of a tile
+
+template <int kFM>
+struct TileOf {
+  static constexpr int kBM = 16 * kFM, kStages = 3;
+  static constexpr int kABytes = kBM * 256, kStage = kABytes + kRowsW * 64;
+  static constexpr int kLoadsA = kABytes / 4096, kLoads = kLoadsA + 2;  // 1 KiB copies of a wavefront and step
+};
+
+template <bool kMx, bool kHalf, int kFM, bool kGated>
+__global__ __launch_bounds__(256, 2) void linear4_tile_kernel(const LinParams p) {
+  typedef TileOf<kFM> Tile;
+  constexpr int kBM = Tile::kBM, kStages = Tile::kStages;
+  constexpr int kOutN = kGated ? kRowsW / 2 : kRowsW;
+  constexpr int kBlocks = kMx ? 4 : 8;                         // block scales of a step and row
+  constexpr int kKind = kHalf ? (int)kF16 : (int)kBf16;
+  __shared__ __align__(1024) char smem[kStages * Tile::kStage];
+  // scales of four steps, two buffers
+  __shared__ __align__(16) uint8_t s_scale[2][kRowsW][4 * kBlocks];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int32_t K = p.kbytes;                                  // (128 elements a step, as work_at counts)
+  const Work work = work_at((int32_t)blockIdx.x, p.tiles_m, p.tiles_n, p.whole, p.parts, p.part_steps, p.kbytes);
+  const int step0 = work.step0, steps = work.steps;
+  const int64_t m0 = (int64_t)work.tm * kBM;
+  const int32_t n0 = work.tn * kOutN;
+
+  // Copies.  a: four rows a copy, 16 chunks of 16 bytes each, chunk c of row r at c ^ (r &
+  // 15); w: 16 rows a copy, four chunks each, at c ^ (r >> 1 & 3).  Rows past the edge
+  // repeat the last one.
+  const char* from_a[Tile::kLoadsA];
+  const char* from_w[2];
+  const int chunk_w = (lane & 3) ^ (lane >> 3 & 3);
+#pragma unroll
+  for (int i = 0; i < Tile::kLoadsA; ++i) {
+    const int r = 4 * (wave * Tile::kLoadsA + i) + (lane >> 4);
+    from_a[i] = p.a + min(m0 + r, (int64_t)p.M - 1) * p.lda + ((lane & 15) ^ (r & 15)) * 16 + (int64_t)step0 * 256;
+  }
+  // (row of the tile -> row of w)
+  auto w_row = [&](int r) { return (int64_t)min(n0 + r % kOutN, p.N - 1) + (r >= kOutN ? p.N : 0); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    from_w[i] = p.w + w_row(16 * (2 * wave + i) + (lane >> 2)) * p.ldw + chunk_w * 16 + (int64_t)step0 * 64;
+  auto fetch = [&](int ks) {
+    char* to = smem + ks % kStages * Tile::kStage;
+    const int32_t left = K - (step0 + ks) * 128;               // elements of the rows from this step on
+#pragma unroll
+    for (int i = 0; i < Tile::kLoadsA; ++i) {
+      const int r = 4 * (wave * Tile::kLoadsA + i) + (lane >> 4), chunk = (lane & 15) ^ (r & 15);
+      char* dst = to + (wave * Tile::kLoadsA + i) * 1024;
+      if (chunk * 8 < left) copy_lds16(reinterpret_cast<uint64_t>(from_a[i]), lds_address(dst));
+      else *reinterpret_cast<u32x4*>(dst + lane * 16) = u32x4{0, 0, 0, 0};
+      from_a[i] += 256;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      char* dst = to + Tile::kABytes + (2 * wave + i) * 1024;
+      if (chunk_w * 32 < left) copy_lds16(reinterpret_cast<uint64_t>(from_w[i]), lds_address(dst));
+      else *reinterpret_cast<u32x4*>(dst + lane * 16) = u32x4{0, 0, 0, 0};
+      from_w[i] += 64;
+    }
+  };
+
+  // scales: two threads a row, two steps each
+  const int scale_of = threadIdx.x >> 1, half = threadIdx.x & 1;
+  const int32_t nblk = K / (kMx ? 32 : 16);
+  const uint8_t* scale_row = static_cast<const uint8_t*>(p.w_scales) + w_row(scale_of) * nblk;
+  struct Scales {
+    uint32_t d[kBlocks / 2];
+  };
+  auto load = [&](int ks) {
+    Scales v;
+    const int at = (step0 + ks + 2 * half) * kBlocks;
+#pragma unroll
+    for (int i = 0; i < kBlocks / 2; i += kBlocks / 4) load_scales4<kMx>(scale_row + min(at + 4 * i, nblk), nblk - at - 4 * i, v.d + i);
+    return v;
+  };
+  auto store = [&](int buf, const Scales& v) {
+#pragma unroll
+    for (int i = 0; i < kBlocks / 2; ++i) *reinterpret_cast<uint32_t*>(&s_scale[buf][scale_of][half * 2 * kBlocks + 4 * i]) = v.d[i];
+  };
+
+  f32x4 acc[kFM][2];
+#pragma unroll
+  for (int i = 0; i < kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  // a wavefront's fragments of w: 32 consecutive rows, or 16 gate rows and their up rows
+  auto w_first = [&](int j) { return kGated ? j * kOutN + wave * 16 : wave * 32 + j * 16; };
+
+  Scales next;
+  auto step = [&](auto tc, int ks) {
+    constexpr int T = decltype(tc)::value;
+    if (ks + kStages - 1 < steps) fetch(ks + kStages - 1);
+    const char* stage = smem + ks % kStages * Tile::kStage;
+    u32x4 w[2];
+    uint32_t s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = w_first(j) + i16;
+      w[j] = *reinterpret_cast<const u32x4*>(stage + Tile::kABytes + r * 64 + ((g ^ (r >> 1 & 3)) << 4));
+      const uint8_t* sc = &s_scale[(ks >> 2) & 1][r][T * kBlocks];
+      if constexpr (kMx) s[j] = sc[g];
+      else s[j] = *reinterpret_cast<const uint16_t*>(sc + 2 * g);
+    }
+    auto part = [&](auto uc) {
+      constexpr int u = decltype(uc)::value;
+      u32x4 wt[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) wt[j] = weights8<kMx, kHalf, kMx ? 0 : u / 2>(w[j][u], s[j]);
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) {
+        const u32x4 a = *reinterpret_cast<const u32x4*>(stage + (i * 16 + i16) * 256 + (((4 * g + u) ^ i16) << 4));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mma4<kMx, kHalf>(wt[j], a, acc[i][j]);
+      }
+    };
+    part(std::integral_constant<int, 0>{});
+    part(std::integral_constant<int, 1>{});
+    part(std::integral_constant<int, 2>{});
+    part(std::integral_constant<int, 3>{});
+    // the next four steps' scales: loaded a step before they go to LDS, which is a step
+    // before they are read
+    if constexpr (T == 1) next = load(ks + 3);
+    if constexpr (T == 2) store(1 - ((ks >> 2) & 1), next);
+    if (ks + kStages - 1 < steps) step_barrier<(kStages - 2) * Tile::kLoads>();
+    else step_barrier<0>();
+  };
+  store(0, load(0));
+#pragma unroll
+  for (int ks = 0; ks < kStages - 1; ++ks)
+    if (ks < steps) fetch(ks);
+  step_barrier<0>();
+  for (int ks = 0;;) {
+    step(std::integral_constant<int, 0>{}, ks);
+    if (++ks == steps) break;
+    step(std::integral_constant<int, 1>{}, ks);
+    if (++ks == steps) break;
+    step(std::integral_constant<int, 2>{}, ks);
+    if (++ks == steps) break;
+    step(std::integral_constant<int, 3>{}, ks);
+    if (++ks == steps) break;
+  }
+
+  // a lane's four results are four consecutive columns of one row
+  if (work.part >= 0) {
+#pragma unroll
+    for (int i = 0; i < kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<f32x4*>(p.partial + partial_at(work.tile - p.whole, work.part, p.parts, i * 16 + i16, w_first(j) + 4 * g, kBM,
+                                                         kRowsW)) = acc[i][j];
+    return;
+  }
+  constexpr int kLd = kRowsW + 4;
+  static_assert(kBM * kLd * 4 <= kStages * Tile::kStage, "the tile fits the step buffers");
+  float* tile = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) *reinterpret_cast<f32x4*>(tile + (i * 16 + i16) * kLd + w_first(j) + 4 * g) = acc[i][j];
+  __syncthreads();
+  constexpr int kPer = kOutN / 8;                              // threads per row
+  const int c = (int)(threadIdx.x % kPer) * 8;
+  const int32_t n = n0 + c;
+  Columns<kKind, kGated, 8> cols;
+  cols.load(p, n);
+#pragma unroll 1
+  for (int r = threadIdx.x / kPer; r < kBM; r += 256 / kPer) {
+    const int64_t m = m0 + r, mr = min(m, (int64_t)p.M - 1);
+    const bool in = m < p.M && n < p.N;
+    Residual<8> res;
+    res.load(p, mr, n);
+    float v[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = tile[r * kLd + c + e];
+      u[e] = tile[r * kLd + c + e + (kGated ? kOutN : 0)];
+    }
+    cols.finish(p, mr, v, u);
+    res.add(p, v);
+    if (p.out_type != kOutBlock8) {
+      if (in) store_run<8>(p, m, n, v);
+    } else {
+      store_block<8>(p, m, n, v, in);
+    }
+  }
+}
+
 // ---- many rows ------------------------------------------------------------------------
 // w in 16 bits, dense rows of `copies` times K elements; a thread writes 32 elements.
 template <bool kMx, bool kHalf>
@@ -239,12 +458,18 @@ __global__ __launch_bounds__(256) void widen4_kernel(const uint8_t* w, int64_t l
   const int64_t row = id / vecs;
   const int32_t v = (int32_t)(id - row * vecs);
   const u32x4 c = *reinterpret_cast<const u32x4*>(w + row * ldw + 16 * v);
-  Scale4<kMx, kHalf> s;
-  if constexpr (kMx) s.set(scales[row * vecs + v]);
-  else s.set(*reinterpret_cast<const uint16_t*>(scales + 2 * (row * vecs + v)));
   u32x4 d[4];
+  if constexpr (kMx) {
+    const uint32_t s = scales[row * vecs + v];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) d[t] = s.weights(c[t], t);
+    for (int t = 0; t < 4; ++t) d[t] = weights8<true, kHalf, 0>(c[t], s);
+  } else {
+    const uint32_t s = *reinterpret_cast<const uint16_t*>(scales + 2 * (row * vecs + v));
+    d[0] = weights8<false, kHalf, 0>(c[0], s);
+    d[1] = weights8<false, kHalf, 0>(c[1], s);
+    d[2] = weights8<false, kHalf, 1>(c[2], s);
+    d[3] = weights8<false, kHalf, 1>(c[3], s);
+  }
   for (int32_t i = 0; i < copies; ++i) {
     u32x4* dst = reinterpret_cast<u32x4*>(out + (row * copies + i) * K + 32 * v);
 #pragma unroll
@@ -267,7 +492,52 @@ __global__ __launch_bounds__(256) void split_rows_kernel(const uint16_t* a, int6
 }
 
 // ---- launches --------------------------------------------------------------------------
-constexpr int32_t kFewRows = 64;
+// Which form: up to 16 rows the first; fp16 against UE8M0 scales, whose split costs too
+// much in every workgroup, up to 64.  Then tiles, cut along K where they leave CUs idle
+// (workspace: the parts' sums), up to kTileRows; more rows are written out.
+constexpr int32_t kFewRows = 16, kFewRowsSplit = 64, kTileRows = 1024;
+
+struct Plan4 {
+  enum { kFew, kTile, kWide } form;
+  int32_t bm, tiles_m, tiles_n, parts, part_steps;
+  size_t bytes;
+};
+
+Plan4 plan4_of(const Linear4Args& a) {
+  Plan4 q = {};
+  const bool split = a.mx && a.kind == kF16;
+  if (a.M <= (split ? kFewRowsSplit : kFewRows)) {
+    q.form = Plan4::kFew;
+    return q;
+  }
+  if (split || a.M > kTileRows) {
+    q.form = Plan4::kWide;
+    return q;
+  }
+  q.form = Plan4::kTile;
+  q.bm = a.M <= 32 ? 32 : 64;
+  q.tiles_m = (a.M - 1) / q.bm + 1;
+  q.tiles_n = (a.N - 1) / (a.gated ? kRowsW / 2 : kRowsW) + 1;
+  const int32_t steps = (a.K + 127) / 128;
+  const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+  q.parts = 1;
+  q.part_steps = steps;
+  float best = 0;
+  for (int32_t parts = 1; parts <= 16 && (parts == 1 || tiles * parts <= 1024); ++parts) {
+    const int32_t each = parts == 1 ? steps : ((steps + parts - 1) / parts + 3) / 4 * 4;  // (scales come in fours)
+    if ((steps + each - 1) / each != parts) continue;
+    const float rounds = (float)((tiles * parts + 511) / 512);
+    float cost = rounds * (each * 0.45f + 3.0f);
+    if (parts > 1) cost += 3.0f + (float)tiles * parts * q.bm * kRowsW * 8.0f / 4e6f;
+    if (best == 0 || cost < best) {
+      best = cost;
+      q.parts = parts;
+      q.part_steps = each;
+      q.bytes = parts > 1 ? (size_t)tiles * parts * q.bm * kRowsW * 4 : 0;
+    }
+  }
+  return q;
+}
 
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
 hipError_t go_few(LinParams p, hipStream_t stream) {
@@ -278,18 +548,42 @@ hipError_t go_few(LinParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool kMx, bool kHalf, int kFM, bool kGated>
+hipError_t go_tile(LinParams p, const Plan4& q, void* workspace, hipStream_t stream) {
+  constexpr int32_t kOutN = kGated ? kRowsW / 2 : kRowsW;
+  const int32_t tiles = q.tiles_m * q.tiles_n;
+  p.kbytes /= 2;                                               // elements
+  p.tiles_m = q.tiles_m;
+  p.tiles_n = q.tiles_n;
+  p.whole = q.parts > 1 ? 0 : tiles;
+  p.parts = q.parts;
+  p.part_steps = q.part_steps;
+  p.partial = static_cast<float*>(workspace);
+  hipLaunchKernelGGL((linear4_tile_kernel<kMx, kHalf, kFM, kGated>), dim3((uint32_t)(tiles * q.parts)), dim3(256), 0, stream, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || q.parts == 1) return err;
+  hipLaunchKernelGGL((linear_join_kernel<kHalf ? (int)kF16 : (int)kBf16, kGated>), dim3((uint32_t)(tiles * (q.bm * (kOutN / 8) / 256))),
+                     dim3(256), 0, stream, p, q.bm, kRowsW);
+  return hipGetLastError();
+}
+
 template <bool kMx, bool kHalf, bool kGated>
-hipError_t go_rows(const LinParams& p, hipStream_t stream) {
+hipError_t go_rows(const LinParams& p, const Plan4& q, void* workspace, hipStream_t stream) {
   constexpr int kFirst = kGated ? 2 : 1;                       // fragments of w for 16 outputs
   const bool block = p.out_type == kOutBlock8;                 // (32 outputs belong together)
   if (p.M <= 16) return block ? go_few<kMx, kHalf, 1, 2 * kFirst, kGated>(p, stream) : go_few<kMx, kHalf, 1, kFirst, kGated>(p, stream);
-  if (p.M <= 32) return go_few<kMx, kHalf, 2, 2 * kFirst, kGated>(p, stream);
-  return go_few<kMx, kHalf, 4, 2 * kFirst, kGated>(p, stream);
+  if constexpr (kMx && kHalf) {
+    if (p.M <= 32) return go_few<kMx, kHalf, 2, 2 * kFirst, kGated>(p, stream);
+    return go_few<kMx, kHalf, 4, 2 * kFirst, kGated>(p, stream);
+  } else {
+    if (q.bm == 32) return go_tile<kMx, kHalf, 2, kGated>(p, q, workspace, stream);
+    return go_tile<kMx, kHalf, 4, kGated>(p, q, workspace, stream);
+  }
 }
 
 template <bool kMx, bool kHalf>
-hipError_t go_gated(const LinParams& p, int32_t gated, hipStream_t stream) {
-  return gated ? go_rows<kMx, kHalf, true>(p, stream) : go_rows<kMx, kHalf, false>(p, stream);
+hipError_t go_gated(const LinParams& p, int32_t gated, const Plan4& q, void* workspace, hipStream_t stream) {
+  return gated ? go_rows<kMx, kHalf, true>(p, q, workspace, stream) : go_rows<kMx, kHalf, false>(p, q, workspace, stream);
 }
 
 // What the many-row form multiplies: a and w in 16 bits.
@@ -318,7 +612,9 @@ Wide wide_of(const Linear4Args& a) {
 }  // namespace
 
 size_t linear4_workspace_bytes(const Linear4Args& a) {
-  if (a.M <= kFewRows || a.N == 0) return 0;
+  if (a.M == 0 || a.N == 0) return 0;
+  const Plan4 plan = plan4_of(a);
+  if (plan.form != Plan4::kWide) return plan.bytes;
   const Wide q = wide_of(a);
   return q.rest_at + linear_workspace_bytes(q.a);
 }
@@ -326,7 +622,8 @@ size_t linear4_workspace_bytes(const Linear4Args& a) {
 hipError_t launch_linear4(const Linear4Args& a, void* workspace, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const bool f16 = a.kind == kF16;
-  if (a.M <= kFewRows) {
+  const Plan4 plan = plan4_of(a);
+  if (plan.form != Plan4::kWide) {
     LinParams p = {};
     p.a = static_cast<const char*>(a.a);
     p.w = static_cast<const char*>(a.w);
@@ -342,8 +639,9 @@ hipError_t launch_linear4(const Linear4Args& a, void* workspace, hipStream_t str
     p.ldo = a.ldo;
     p.M = a.M; p.N = a.N; p.kbytes = a.K * 2;
     p.act = a.act; p.bias_type = a.bias_type; p.residual_type = a.residual_type; p.out_type = a.out_type;
-    if (a.mx) return f16 ? go_gated<true, true>(p, a.gated, stream) : go_gated<true, false>(p, a.gated, stream);
-    return f16 ? go_gated<false, true>(p, a.gated, stream) : go_gated<false, false>(p, a.gated, stream);
+    if (a.mx)
+      return f16 ? go_gated<true, true>(p, a.gated, plan, workspace, stream) : go_gated<true, false>(p, a.gated, plan, workspace, stream);
+    return f16 ? go_gated<false, true>(p, a.gated, plan, workspace, stream) : go_gated<false, false>(p, a.gated, plan, workspace, stream);
   }
   Wide q = wide_of(a);
   char* ws = static_cast<char*>(workspace);
