@@ -12,9 +12,10 @@
 // are split into two bf16 numbers, the upper 8 of their 11 bits and the lower 3, which
 // are multiplied apart: every product is exact and the sums are fp32 sums.
 //
-// Few rows (at most 64) are bound by reading w once and go from memory to registers:
-// linear4_few_kernel.  More rows are bound by the matrix units: w is written out in 16
-// bits once (4.5 bits read and 16 written an element) and the linear operator's tiles
+// Few rows are bound by reading w once and go from memory to registers
+// (linear4_few_kernel).  More rows would read a too often so: tiles, with a and w's codes in
+// LDS, widen w once for 16 to 128 rows of a (linear4_tile_kernel).  Many rows are bound by
+// the matrix units: w is written out in 16 bits once and the linear operator's tiles
 // multiply it.
 #include "internal.h"
 #include "linear_kernels.h"
@@ -83,11 +84,10 @@ __device__ __forceinline__ f32x4 mma4(const u32x4& w, const u32x4& a, f32x4 acc)
 // ---- few rows -------------------------------------------------------------------
 // A workgroup owns 16 * kFN rows of w (gated: gate rows, then up rows) and 16 * kRF rows
 // of a.  Its wavefronts take groups of 128 elements of K in turn, kBatch groups' loads in
-// flight at once.  The t-th of a group's four matrix instructions takes elements 32 t ..
-// 32 t + 31, lane group g eight from 8 g on: a's loads are then 64 bytes of a row in one
-// piece.  w comes 16 bytes a lane, 32 elements, and four lane groups exchange words, so
-// that each has its run of all four.  The wavefronts' sums are added in order through
-// LDS, 16 rows at a time.
+// flight at once and the next ones' w on its way: a lane's 16 bytes of w are 32 elements
+// of a row, the next 32 belong to the next group of 16 lanes, and the four matrix
+// instructions of a group take 8 elements of each (any order of K that both operands
+// share).  The wavefronts' sums are added in order through LDS, 16 rows at a time.
 //
 // The block scales of 128 elements of a row, `blocks` of them inside it (a multiple of 32
 // elements): 8 bytes of E4M3 at an even address, or 4 of UE8M0 at any.  Those past the
@@ -106,20 +106,10 @@ __device__ __forceinline__ void load_scales4(const uint8_t* at, int32_t blocks, 
     if (i < blocks) s[i / 4] |= (uint32_t)at[i] << (8 * (i % 4));
 }
 
-// Word g of the 16 bytes that lane group t loaded, in d[t] of lane group g: a transpose
-// of four words across the four groups of 16 lanes.
-__device__ __forceinline__ u32x4 exchange(const u32x4& w) {
-  const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);   // upper half of one, lower half of the other
-  const auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);  // odd groups of one, even ones of the other
-  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  return u32x4{c[0], c[1], d[0], d[1]};
-}
-
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
 __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
   constexpr int kWaves = 8, kRows = 16 * kFN, kCols = kGated ? kRows / 2 : kRows;
-  constexpr int kBatch = kRF * kFN <= 2 ? 4 : kRF <= 2 ? 2 : 1;
+  constexpr int kBatch = kRF * kFN <= 2 ? 2 : 1;
   constexpr int kLd = kRows + 4;                               // floats per row of a partial tile
   constexpr bool kSplit = kMx && kHalf;
   constexpr int kBlock = kMx ? 32 : 16;
@@ -151,45 +141,50 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
     for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
   const int groups = (K + 127) / 128;
-  for (int first = kBatch * wave; first < groups; first += kBatch * kWaves) {
-    u32x4 w[kBatch][kFN], a[kBatch][kRF][4];
-    uint32_t s[kBatch][kFN][kMx ? 1 : 2];
+  struct Weights {
+    u32x4 w[kBatch][kFN];
+    uint32_t s[kBatch][kFN];                                   // a lane's two E4M3 codes or one UE8M0 code
+  };
+  // past the end of a row codes, scales and a count as zeros
+  auto load_w = [&](int first, Weights& q) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      // past the end of a row codes, scales and a count as zeros
-      const int32_t k0 = (first + b) * 128;
-      const int32_t blocks = (K - k0) / kBlock;                // (0 or less: none)
+      const int32_t k = (first + b) * 128 + 32 * g;
 #pragma unroll
       for (int j = 0; j < kFN; ++j) {
-        w[b][j] = u32x4{0, 0, 0, 0};
-        if (k0 + 32 * g < K) w[b][j] = *reinterpret_cast<const u32x4*>(pw[j] + k0 / 2 + 16 * g);
-        load_scales4<kMx>(sw[j] + k0 / kBlock, blocks, s[b][j]);
+        q.w[b][j] = u32x4{0, 0, 0, 0};
+        q.s[b][j] = 0;
+        if (k < K) {
+          q.w[b][j] = *reinterpret_cast<const u32x4*>(pw[j] + k / 2);
+          if constexpr (kMx) q.s[b][j] = sw[j][k / 32];
+          else q.s[b][j] = *reinterpret_cast<const uint16_t*>(sw[j] + k / 16);
+        }
       }
+    }
+  };
+  Weights now, next;
+  load_w(kBatch * wave, now);
+  for (int first = kBatch * wave; first < groups; first += kBatch * kWaves) {
+    load_w(first + kBatch * kWaves, next);
+    u32x4 a[kBatch][kRF][4];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int32_t k = (first + b) * 128 + 32 * g;
 #pragma unroll
       for (int i = 0; i < kRF; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           a[b][i][t] = u32x4{0, 0, 0, 0};
-          if (k0 + 32 * t < K) a[b][i][t] = *reinterpret_cast<const u32x4*>(pa[i] + 2 * (k0 + 32 * t + 8 * g));
+          if (k < K) a[b][i][t] = *reinterpret_cast<const u32x4*>(pa[i] + 2 * k + 16 * t);
         }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      u32x4 c[kFN];
-#pragma unroll
-      for (int j = 0; j < kFN; ++j) {
-        c[j] = exchange(w[b][j]);
-        // E4M3: lane groups 0 and 1 take the even blocks, 2 and 3 the odd ones
-        if constexpr (!kMx) {
-          s[b][j][0] >>= 8 * (g >> 1);
-          s[b][j][1] >>= 8 * (g >> 1);
-        }
-      }
       auto part = [&](auto tc) {
         constexpr int t = decltype(tc)::value;
         u32x4 wt[kFN];
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) wt[j] = weights8<kMx, kHalf, kMx ? t : t % 2 * 2>(c[j][t], s[b][j][kMx ? 0 : t / 2]);
+        for (int j = 0; j < kFN; ++j) wt[j] = weights8<kMx, kHalf, kMx ? 0 : t / 2>(now.w[b][j][t], now.s[b][j]);
 #pragma unroll
         for (int i = 0; i < kRF; ++i) {
           if constexpr (kSplit) {
@@ -210,6 +205,7 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
       part(std::integral_constant<int, 2>{});
       part(std::integral_constant<int, 3>{});
     }
+    now = next;
   }
 
   constexpr int kKind = kHalf ? (int)kF16 : (int)kBf16;
@@ -258,19 +254,18 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
 // step and w as codes; a wavefront widens its own rows of w, once for all rows of a.  Lane
 // group g holds elements 32 g .. 32 g + 31 of a step, the t-th matrix instruction takes
 // eight of them.
-constexpr int kRowsW = 128;                                    // rows of w of a tile
-
-template <int kFM>
+template <int kFM, int kWaves>
 struct TileOf {
-  static constexpr int kBM = 16 * kFM, kStages = 3;
+  static constexpr int kBM = 16 * kFM, kRowsW = 32 * kWaves, kThreads = 64 * kWaves;
   static constexpr int kABytes = kBM * 256, kStage = kABytes + kRowsW * 64;
-  static constexpr int kLoadsA = kABytes / 4096, kLoads = kLoadsA + 2;  // 1 KiB copies of a wavefront and step
+  static constexpr int kLoadsA = kABytes / (1024 * kWaves), kLoads = kLoadsA + 2;  // 1 KiB copies of a wavefront and step
+  static constexpr int kStages = kFM == 1 ? 5 : kFM == 2 ? 4 : 3;
 };
 
-template <bool kMx, bool kHalf, int kFM, bool kGated>
-__global__ __launch_bounds__(256, 2) void linear4_tile_kernel(const LinParams p) {
-  typedef TileOf<kFM> Tile;
-  constexpr int kBM = Tile::kBM, kStages = Tile::kStages;
+template <bool kMx, bool kHalf, int kFM, int kWaves, bool kGated>
+__global__ __launch_bounds__(64 * kWaves, 2) void linear4_tile_kernel(const LinParams p) {
+  typedef TileOf<kFM, kWaves> Tile;
+  constexpr int kBM = Tile::kBM, kStages = Tile::kStages, kRowsW = Tile::kRowsW, kThreads = Tile::kThreads;
   constexpr int kOutN = kGated ? kRowsW / 2 : kRowsW;
   constexpr int kBlocks = kMx ? 4 : 8;                         // block scales of a step and row
   constexpr int kKind = kHalf ? (int)kF16 : (int)kBf16;
@@ -426,7 +421,7 @@ __global__ __launch_bounds__(256, 2) void linear4_tile_kernel(const LinParams p)
   Columns<kKind, kGated, 8> cols;
   cols.load(p, n);
 #pragma unroll 1
-  for (int r = threadIdx.x / kPer; r < kBM; r += 256 / kPer) {
+  for (int r = threadIdx.x / kPer; r < kBM; r += kThreads / kPer) {
     const int64_t m = m0 + r, mr = min(m, (int64_t)p.M - 1);
     const bool in = m < p.M && n < p.N;
     Residual<8> res;
@@ -492,51 +487,78 @@ __global__ __launch_bounds__(256) void split_rows_kernel(const uint16_t* a, int6
 }
 
 // ---- launches --------------------------------------------------------------------------
-// Which form: up to 16 rows the first; fp16 against UE8M0 scales, whose split costs too
-// much in every workgroup, up to 64.  Then tiles, cut along K where they leave CUs idle
-// (workspace: the parts' sums), up to kTileRows; more rows are written out.
-constexpr int32_t kFewRows = 16, kFewRowsSplit = 64, kTileRows = 1024;
-
+// Which form: fp16 against UE8M0 scales, whose split costs too much in every workgroup,
+// takes the first up to 64 rows and the last beyond.
 struct Plan4 {
   enum { kFew, kTile, kWide } form;
-  int32_t bm, tiles_m, tiles_n, parts, part_steps;
+  int32_t fm, bm, rows_w, tiles_m, tiles_n, whole, parts, part_steps;
   size_t bytes;
+  float cost;
 };
 
-Plan4 plan4_of(const Linear4Args& a) {
+// Tiles that fill whole rounds of the CUs are computed whole, those of the last round cut
+// along K, as the linear operator's (plan_of).
+Plan4 tile4_plan(const Linear4Args& a, int fm, int waves, int32_t slots, float step, float rest) {
   Plan4 q = {};
-  const bool split = a.mx && a.kind == kF16;
-  if (a.M <= (split ? kFewRowsSplit : kFewRows)) {
-    q.form = Plan4::kFew;
-    return q;
-  }
-  if (split || a.M > kTileRows) {
-    q.form = Plan4::kWide;
-    return q;
-  }
   q.form = Plan4::kTile;
-  q.bm = a.M <= 32 ? 32 : 64;
+  q.fm = fm;
+  q.bm = 16 * fm;
+  q.rows_w = 32 * waves;
   q.tiles_m = (a.M - 1) / q.bm + 1;
-  q.tiles_n = (a.N - 1) / (a.gated ? kRowsW / 2 : kRowsW) + 1;
+  q.tiles_n = (a.N - 1) / (a.gated ? q.rows_w / 2 : q.rows_w) + 1;
   const int32_t steps = (a.K + 127) / 128;
-  const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-  q.parts = 1;
-  q.part_steps = steps;
-  float best = 0;
-  for (int32_t parts = 1; parts <= 16 && (parts == 1 || tiles * parts <= 1024); ++parts) {
+  const int64_t total = (int64_t)q.tiles_m * q.tiles_n;
+  const int32_t left = (int32_t)(total % slots);
+  const float rounds = (float)(total / slots) * (steps * step + rest);
+  for (int32_t parts = 1; parts <= (left ? (slots / left < 16 ? slots / left : 16) : 1); ++parts) {
     const int32_t each = parts == 1 ? steps : ((steps + parts - 1) / parts + 3) / 4 * 4;  // (scales come in fours)
     if ((steps + each - 1) / each != parts) continue;
-    const float rounds = (float)((tiles * parts + 511) / 512);
-    float cost = rounds * (each * 0.45f + 3.0f);
-    if (parts > 1) cost += 3.0f + (float)tiles * parts * q.bm * kRowsW * 8.0f / 4e6f;
-    if (best == 0 || cost < best) {
-      best = cost;
+    float cost = rounds;
+    if (left) cost += each * step + rest;
+    if (parts > 1) cost += 3.0f + (float)left * parts * q.bm * q.rows_w * 8.0f / 4e6f;
+    if (q.cost == 0 || cost < q.cost) {
+      q.cost = cost;
       q.parts = parts;
       q.part_steps = each;
-      q.bytes = parts > 1 ? (size_t)tiles * parts * q.bm * kRowsW * 4 : 0;
+      q.whole = (int32_t)(parts > 1 ? total - left : total);
+      q.bytes = parts > 1 ? (size_t)left * parts * q.bm * q.rows_w * 4 : 0;
     }
   }
   return q;
+}
+
+// Forms' costs in us, by measured rates, and the least of them.  Few rows: w at 3 MB/us,
+// and a again for every 16 rows of w at 14 MB/us from L2.  Tiles of 16, 32, 64 and 128 rows:
+// a step is bound by widening w (E4M3 to bf16 16 instructions for 8 elements of a lane, to
+// fp16 8, UE8M0 4).  Written out: 2.5 bytes an element at 5.3 MB/us, then the linear
+// operator.  Forms measured against each other, in us, at 8192 x 8192 with E4M3 scales in
+// bf16 (few, tiles of 16, 32, 64, 128, written out): 1 row 17, 19, 22, 29, 47, 71; 16 rows
+// 26, 20, 21, 28, 47, 81; 64 rows -, 38, 27, 28, 46, 80; 256 rows -, 119, 66, 58, 51, 118;
+// 1024 rows -, 448, 245, 184, 141, 174.  4096 x (2 x 2112) x 2816: 64-row tiles 142, 128-row
+// tiles 130, written out 114.
+Plan4 plan4_of(const Linear4Args& a) {
+  Plan4 few = {}, wide = {};
+  few.form = Plan4::kFew;
+  wide.form = Plan4::kWide;
+  if (a.mx && a.kind == kF16) return a.M <= 64 ? few : wide;
+  const float rows = a.gated ? 2.0f * a.N : (float)a.N, weights = rows * a.K;
+  const int c = a.mx ? 2 : a.kind == kF16 ? 1 : 0;
+  static const float kStepUs[4][3] = {{0.9f, 0.76f, 0.58f}, {0.95f, 0.8f, 0.74f}, {1.38f, 1.27f, 1.08f}, {2.1f, 2.0f, 1.87f}};
+  Plan4 best = tile4_plan(a, 1, 4, 512, kStepUs[0][c], 7.0f);
+  auto take = [&](const Plan4& q) {
+    if (q.cost < best.cost) best = q;
+  };
+  if (a.M > 16) take(tile4_plan(a, 2, 4, 512, kStepUs[1][c], 7.0f));
+  if (a.M > 32) take(tile4_plan(a, 4, 4, 512, kStepUs[2][c], 6.0f));
+  if (a.M > 64) take(tile4_plan(a, 8, 8, 256, kStepUs[3][c], 10.0f));
+  if (a.M <= 16) {
+    few.cost = 4.0f + weights * 0.5625f / 3e6f + weights / 16 * a.M * 2 / 14e6f;
+    take(few);
+  } else {
+    wide.cost = 6.0f + weights * 2.5f / 5.3e6f + plan_of(a.M, a.N, 2 * a.K, a.kind, a.gated != 0).cost;
+    take(wide);
+  }
+  return best;
 }
 
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
@@ -548,22 +570,23 @@ hipError_t go_few(LinParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool kMx, bool kHalf, int kFM, bool kGated>
+template <bool kMx, bool kHalf, int kFM, int kWaves, bool kGated>
 hipError_t go_tile(LinParams p, const Plan4& q, void* workspace, hipStream_t stream) {
-  constexpr int32_t kOutN = kGated ? kRowsW / 2 : kRowsW;
-  const int32_t tiles = q.tiles_m * q.tiles_n;
+  const int32_t out_n = kGated ? q.rows_w / 2 : q.rows_w;
+  const int32_t left = q.tiles_m * q.tiles_n - q.whole;
   p.kbytes /= 2;                                               // elements
   p.tiles_m = q.tiles_m;
   p.tiles_n = q.tiles_n;
-  p.whole = q.parts > 1 ? 0 : tiles;
+  p.whole = q.whole;
   p.parts = q.parts;
   p.part_steps = q.part_steps;
   p.partial = static_cast<float*>(workspace);
-  hipLaunchKernelGGL((linear4_tile_kernel<kMx, kHalf, kFM, kGated>), dim3((uint32_t)(tiles * q.parts)), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((linear4_tile_kernel<kMx, kHalf, kFM, kWaves, kGated>), dim3((uint32_t)(q.whole + left * q.parts)), dim3(64 * kWaves), 0,
+                     stream, p);
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || q.parts == 1) return err;
-  hipLaunchKernelGGL((linear_join_kernel<kHalf ? (int)kF16 : (int)kBf16, kGated>), dim3((uint32_t)(tiles * (q.bm * (kOutN / 8) / 256))),
-                     dim3(256), 0, stream, p, q.bm, kRowsW);
+  if (err != hipSuccess || left == 0) return err;
+  hipLaunchKernelGGL((linear_join_kernel<kHalf ? (int)kF16 : (int)kBf16, kGated>), dim3((uint32_t)(((int64_t)left * q.bm * (out_n / 8) + 255) / 256)),
+                     dim3(256), 0, stream, p, q.bm, q.rows_w);
   return hipGetLastError();
 }
 
@@ -571,14 +594,20 @@ template <bool kMx, bool kHalf, bool kGated>
 hipError_t go_rows(const LinParams& p, const Plan4& q, void* workspace, hipStream_t stream) {
   constexpr int kFirst = kGated ? 2 : 1;                       // fragments of w for 16 outputs
   const bool block = p.out_type == kOutBlock8;                 // (32 outputs belong together)
-  if (p.M <= 16) return block ? go_few<kMx, kHalf, 1, 2 * kFirst, kGated>(p, stream) : go_few<kMx, kHalf, 1, kFirst, kGated>(p, stream);
-  if constexpr (kMx && kHalf) {
-    if (p.M <= 32) return go_few<kMx, kHalf, 2, 2 * kFirst, kGated>(p, stream);
-    return go_few<kMx, kHalf, 4, 2 * kFirst, kGated>(p, stream);
-  } else {
-    if (q.bm == 32) return go_tile<kMx, kHalf, 2, kGated>(p, q, workspace, stream);
-    return go_tile<kMx, kHalf, 4, kGated>(p, q, workspace, stream);
+  if (q.form == Plan4::kFew) {
+    if (p.M <= 16) return block ? go_few<kMx, kHalf, 1, 2 * kFirst, kGated>(p, stream) : go_few<kMx, kHalf, 1, kFirst, kGated>(p, stream);
+    if constexpr (kMx && kHalf) {
+      if (p.M <= 32) return go_few<kMx, kHalf, 2, 2 * kFirst, kGated>(p, stream);
+      return go_few<kMx, kHalf, 4, 2 * kFirst, kGated>(p, stream);
+    }
   }
+  if constexpr (!(kMx && kHalf)) {
+    if (q.fm == 1) return go_tile<kMx, kHalf, 1, 4, kGated>(p, q, workspace, stream);
+    if (q.fm == 2) return go_tile<kMx, kHalf, 2, 4, kGated>(p, q, workspace, stream);
+    if (q.fm == 4) return go_tile<kMx, kHalf, 4, 4, kGated>(p, q, workspace, stream);
+    return go_tile<kMx, kHalf, 8, 8, kGated>(p, q, workspace, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <bool kMx, bool kHalf>

@@ -1082,7 +1082,8 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
 template <int kKind, bool kGated>
 __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int32_t bm, int32_t bn) {
   const int32_t out_n = kGated ? bn / 2 : bn, per = out_n / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;   // bm * per is a multiple of 256
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)(p.tiles_m * p.tiles_n - p.whole) * bm * per) return;  // whole rows of a tile
   const int32_t c = (int32_t)(id % per) * 8;
   const int32_t r = (int32_t)(id / per % bm);
   const int32_t left = (int32_t)(id / ((int64_t)per * bm));

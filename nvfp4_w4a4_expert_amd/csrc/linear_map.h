@@ -34,6 +34,7 @@ struct Plan {
   int32_t tile, tiles_m, tiles_n;
   int32_t whole, parts, part_steps;
   uint64_t bytes;                                              // workspace
+  float cost;                                                  // us, by the rates below
 };
 
 // What a launch takes, by measured rates in us: `step` per K step of a round (all
@@ -60,7 +61,7 @@ inline Rate rate_of(int kind, int kernel) {
 // x 2816 bf16: 64 tiles in 4 parts 15.6 / 18.2 (chosen), uncut 17.1 / 18.4; 128 tiles in
 // 6 parts 18.9 / 22.0, uncut 27.2 / 51.
 inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) {
-  if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0};
+  if (M <= 16) return {kFew, 0, 0, 0, 0, 0, 0, 0, 0};
   const int32_t steps = (kbytes + kStep - 1) / kStep;
   Plan best = {};
   float best_cost = 0;
@@ -69,7 +70,7 @@ inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) 
     const int32_t out_n = gated ? tile / 2 : tile;
     const int32_t slots = kernel == kTile256 ? 256 : 512;
     const int32_t threads = kernel == kTile256 ? 512 : 256;
-    Plan q = {kernel, tile, (M - 1) / tile + 1, (N - 1) / out_n + 1, 0, 1, steps, 0};
+    Plan q = {kernel, tile, (M - 1) / tile + 1, (N - 1) / out_n + 1, 0, 1, steps, 0, 0};
     // a launch holds at most 2^32 - 1 threads (the callers' limit on sizes leaves
     // room for tiles of 128)
     if ((int64_t)q.tiles_m * q.tiles_n > 0x7FFFFFFF / threads) continue;
@@ -88,6 +89,7 @@ inline Plan plan_of(int32_t M, int32_t N, int32_t kbytes, int kind, bool gated) 
       if (best_cost == 0 || cost < best_cost) {
         best_cost = cost;
         best = q;
+        best.cost = cost;
         best.parts = parts;
         best.part_steps = each;
         best.whole = parts > 1 ? total - left : total;
