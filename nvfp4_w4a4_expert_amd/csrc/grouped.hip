@@ -4,10 +4,11 @@
 //   out[m, n] = act(sum_k a[row(m), k] * w[e, n, k] + bias[e, n]),   offsets[e] <= m < offsets[e + 1],
 //
 // or act(gate) * up.  The groups' sizes stay on the device: the grid covers the most
-// tiles that M rows can fall into, each workgroup finds its expert from the offsets
-// (0.5 us, by a prefix over the experts in every wavefront), those without a tile end.
-// A tile belongs to one expert, so a group's last tile is partly empty; rows of a are
-// gathered by the copies into LDS themselves.
+// tiles that M rows can fall into, each workgroup finds its expert from the offsets (2 us
+// with the start of the kernel, by prefixes over the experts in every wavefront), those
+// without a tile end.  A tile belongs to one expert, so a group's last tile is partly
+// empty: it leaves out the instructions, copies and epilogue of its empty rows and keeps
+// more steps on their way.  Rows of a are gathered by the copies into LDS themselves.
 #include "internal.h"
 #include "linear_kernels.h"
 
@@ -21,19 +22,10 @@ hipError_t go_tile(const GroupParams& p, uint32_t blocks, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int kKind, int kCols, bool kGated>
-hipError_t go_few(const GroupParams& p, uint32_t blocks, hipStream_t stream) {
-  hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 8, kGated, true>), dim3(blocks), dim3(512), 0, stream, p);
-  return hipGetLastError();
-}
-
 template <int kKind, bool kGated>
 hipError_t go(GroupParams p, const GroupPlan& plan, hipStream_t stream) {
   const uint32_t blocks = (uint32_t)group_blocks(plan.row_tiles, plan.tiles_n);
   p.tiles_n = plan.tiles_n;
-  if constexpr (kKind != kRow8 && kKind != kBlock8)
-    if (plan.kernel == kFew)
-      return p.out_type == kOutBlock8 ? go_few<kKind, 32, kGated>(p, blocks, stream) : go_few<kKind, 16, kGated>(p, blocks, stream);
   if constexpr (!is_wide(kKind))
     if (plan.kernel == kTile256) return go_tile<kKind, 256, 2, 4, 2, kGated>(p, blocks, stream);
   if (plan.kernel == kTile128) return go_tile<kKind, 128, 2, 2, 2, kGated>(p, blocks, stream);
@@ -80,7 +72,7 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {
   p.bias_each = rows;
   p.experts = a.experts; p.a_rows = a.a_rows; p.index_div = a.index_div;
   const GroupPlan plan = plan_for(a);
-  switch (kind_of(a.kind, plan.kernel == kFew ? 16 : 17, a.out_type)) {
+  switch (kind_of(a.kind, 17, a.out_type)) {
     case kBf16: return go_gated<kBf16>(p, a.gated, plan, stream);
     case kF16: return go_gated<kF16>(p, a.gated, plan, stream);
     case kRow8: return go_gated<kRow8>(p, a.gated, plan, stream);

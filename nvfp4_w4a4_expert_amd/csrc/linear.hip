@@ -53,9 +53,9 @@ hipError_t go_few(const LinParams& p, hipStream_t stream) {
   const uint32_t blocks = (uint32_t)((p.N + kCols - 1) / kCols);
   // up to a workgroup per CU: 16 wavefronts, where there are steps for them
   if (blocks <= 256 && p.kbytes > 32 * kStep)
-    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 16, kGated, false>), dim3(blocks), dim3(1024), 0, stream, p);
+    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 16, kGated>), dim3(blocks), dim3(1024), 0, stream, p);
   else
-    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 8, kGated, false>), dim3(blocks), dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((linear_few_kernel<kKind, kCols, 8, kGated>), dim3(blocks), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -652,10 +652,10 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   constexpr bool kScaled = is_block8(kKind);
   static_assert(kBM + kBN <= 64 * kWaves || !kScaled, "a thread loads the scales of one row");
   static_assert((kStages & (kStages - 1)) == 0, "buffer of a step by masking");
-  // Grouped 256-row tiles: a group's last tile has few rows of a to keep, and w for it
-  // comes from memory, so its steps get as many buffers as LDS holds.
-  constexpr bool kDeep = kGroup && kBM == 256;
-  constexpr int kSmem = kDeep ? 160 * 1024 - (kScaled ? 2 * (kBM + kBN) * 16 : 0) : kStages * kStage;
+  // Grouped: a group's last tile has few rows of a to keep, and w for it comes from memory,
+  // so its steps get as many buffers as LDS holds (two workgroups of 128-row tiles a CU).
+  constexpr bool kDeep = kGroup && kBM >= 128 && !is_wide(kKind);
+  constexpr int kSmem = !kDeep ? kStages * kStage : kBM == 256 ? 160 * 1024 - (kScaled ? 2 * (kBM + kBN) * 16 : 0) : 72 * 1024;
   __shared__ __align__(1024) char smem[kSmem];
   __shared__ __align__(16) uint32_t s_scale[kScaled ? 2 : 1][kScaled ? kBM + kBN : 1][4];
 
@@ -717,15 +717,16 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   if constexpr (kDeep) {
     const int rows = last_row_of(kBM, p.M, m0) + 1;
     if (rows <= kBM / 2) {
-      a_bytes = (rows <= kBM / 4 ? kBM / 4 : kBM / 2) * kStep;
+      const bool quarter = kBM == 256 && rows <= kBM / 4;
+      a_bytes = (quarter ? kBM / 4 : kBM / 2) * kStep;
       stage = a_bytes + kBN * kStep;
-      ring = rows <= kBM / 4 && !kScaled ? 4 : 3;
+      ring = quarter && !kScaled ? 4 : 3;
     }
   }
   // (a wavefront copies all rows of its part or, behind the last row, none: step_barrier
   // counts copies)
   const int my_part = wave * kLoads * 1024 - (from.of_a ? 0 : kBM * kStep - a_bytes);
-  const bool mine = !kDeep || !from.of_a || __builtin_amdgcn_readfirstlane(row0) <= last_row;
+  const bool mine = !kGroup || !from.of_a || __builtin_amdgcn_readfirstlane(row0) <= last_row;
   // step ks's copies, into the buffer at `at`
   auto fetch = [&](int ks, int at) {
     if (!mine) {
@@ -878,7 +879,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     // behind the barrier this buffer is read and the next one filled; copies that
     // are on their way then are those of the steps from ks + 2 on
     if (kStages > 2 && ks + kStages <= steps) step_barrier<(kStages - 2) * kLoads>();
-    else if (kDeep && ring == 4 && ks + 4 <= steps) step_barrier<2 * kLoads>();
+    else if (kDeep && kBM == 256 && ring == 4 && ks + 4 <= steps) step_barrier<2 * kLoads>();
     else if (kDeep && ring == 3 && ks + 3 <= steps) step_barrier<kLoads>();
     else step_barrier<0>();
     if (!kLate && ks + ring < steps) fetch(ks + ring, here);
@@ -1131,8 +1132,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
 // top); with w in the last-level cache 25.0, 14.3 and 19.9.  Small products are bound by
 // a launch and one round of loads: 5 x 2816 x 2112 in 4.7 us, 16 x 128 x 2816 in 7.2,
 // whose eight workgroups each read 180 kB.
-template <int kKind, int kCols, int kWaves, bool kGated, bool kGroup>
-__global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const ParamsOf<kGroup> given) {
+template <int kKind, int kCols, int kWaves, bool kGated>
+__global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const LinParams p) {
   constexpr int kRows = kGated ? 2 * kCols : kCols;            // rows of w
   constexpr int kFN = kRows / 16;
   // steps in flight: what 64 (16 wavefronts) or 128 kB of registers hold
@@ -1141,16 +1142,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const ParamsOf<
   __shared__ __align__(16) float part[kWaves][16][kLd];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  ParamsOf<kGroup> p = given;
-  int64_t m0 = 0;
-  int32_t n0 = (int32_t)blockIdx.x * kCols;
-  if constexpr (kGroup) {
-    const GroupTile tile = group_tile(given, (int32_t)blockIdx.x, 16);
-    if (tile.expert < 0) return;
-    take_expert(p, tile);
-    m0 = tile.first + (int64_t)tile.tm * 16;
-    n0 = tile.tn * kCols;
-  }
+  const int32_t n0 = (int32_t)blockIdx.x * kCols;
   const int32_t nblk = p.kbytes / 32;
 
   const char* pw[kFN];
@@ -1164,7 +1156,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const ParamsOf<
     pw[j] = p.w + row * p.ldw;
     sw[j] = static_cast<const uint8_t*>(p.w_scales) + row * nblk;
   }
-  const int64_t row = max(a_row_of(p, min(m0 + i16, (int64_t)p.M - 1)), (int64_t)0);
+  const int64_t row = i16 < p.M ? i16 : p.M - 1;
   const char* pa = p.a + row * p.lda;
   const uint8_t* sa = static_cast<const uint8_t*>(p.a_scales) + row * nblk;
   f32x4 acc[kFN];
@@ -1235,18 +1227,17 @@ __global__ __launch_bounds__(64 * kWaves) void linear_few_kernel(const ParamsOf<
       v += *reinterpret_cast<const f32x4*>(&part[w][r][c]);
       if constexpr (kGated) u += *reinterpret_cast<const f32x4*>(&part[w][r][kCols + c]);
     }
-    const int64_t m = m0 + r;
+    const int64_t m = r;
     const int32_t n = n0 + c;
-    const int64_t ma = a_row_of(p, min(m, (int64_t)p.M - 1));
-    const bool in = m < p.M && n < p.N && ma >= 0;
+    const bool in = m < p.M && n < p.N;
     float gv[4] = {v.x, v.y, v.z, v.w}, uv[4] = {u.x, u.y, u.z, u.w};
-    const int64_t mr = max(ma, (int64_t)0);
+    const int64_t mr = m < p.M ? m : (int64_t)p.M - 1;
     Columns<kKind, kGated, 4> cols;
     cols.load(p, n);
     cols.finish(p, mr, gv, uv);
     Residual<4> res;
-    if constexpr (!kGroup) res.load(p, mr, n);
-    if constexpr (!kGroup) res.add(p, gv);
+    res.load(p, mr, n);
+    res.add(p, gv);
     if (p.out_type != kOutBlock8) {
       if (in) store_run<4>(p, m, n, gv);
     } else if constexpr (kCols % 32 == 0) {

@@ -109,9 +109,18 @@ inline int kind_of(int kind, int32_t M, int32_t out_type) {
   return kind == kRow8 ? kRow8Wide : kBlock8Wide;
 }
 
-// The kernel of a product grouped by expert: M rows over `experts` groups of sizes that
-// only the device knows.  row_tiles is the most tiles (of 16 rows for the few-row form)
-// that M rows can fall into; tiles beyond those in use end at once.
+// The tile of a product grouped by expert: M rows over `experts` groups of sizes that only
+// the device knows.  row_tiles is the most tiles that M rows can fall into; workgroups
+// beyond those in use end at once.
+//
+// 256-row tiles where the groups fill them on average, 128-row tiles where there are
+// enough for the chip, else 64-row tiles; with long rows and few of them 64-row tiles too,
+// whose four buffers cover more of the memory's latency.  Measured as 64 / 128 / 256, us,
+// a router with likes, 128 experts, hidden 2816, intermediate 704, top-8: gate/up in bf16 of
+// 1 token 18 / 32 / -, 4: 28 / 45 / -, 16: 56 / 56 / -, 64: 75 / 86 / -, 256: 113 / 119 / -,
+// 512: 150 / 129 / 163, 1024: 219 / 181 / 200, 2048: 359 / 271 / 265, 4096: 615 / 393 / 382;
+// with block scales 16: 42 / 35 / -, 256: 90 / 76 / -, 4096: 493 / 252 / 236; down in bf16 of
+// 16: 40 / 33 / -, 256: 79 / 67 / -.  8 experts, top-2, 333 x 1411 x 704 fp16 12.5 / 17 / 36.
 struct GroupPlan {
   int kernel;
   int32_t tile, tiles_n;
@@ -120,11 +129,23 @@ struct GroupPlan {
 
 inline GroupPlan group_plan_of(int32_t M, int32_t experts, int32_t N, int32_t kbytes, int kind, bool gated, int out_type) {
   const int32_t groups = M < experts ? M : experts, mean = M / groups;
+  // about how many tiles: half a tile's rows of each group are empty
+  auto tiles = [&](int32_t tile) {
+    const int64_t rows = M / tile + groups / 2;
+    return (rows > groups ? rows : groups) * ((N - 1) / (gated ? tile / 2 : tile) + 1);
+  };
   GroupPlan q;
-  q.kernel = mean <= 16 ? kFew : mean <= 96 ? kTile64 : is_wide(kind_of(kind, 17, out_type)) ? kTile128 : kTile256;
-  q.tile = q.kernel == kFew ? 16 : q.kernel == kTile64 ? 64 : q.kernel == kTile128 ? 128 : 256;
-  const int32_t columns = q.kernel == kFew ? (out_type == kOutBlock8 ? 32 : 16) : gated ? q.tile / 2 : q.tile;
-  q.tiles_n = (N - 1) / columns + 1;
+  if (mean >= 128 && !is_wide(kind_of(kind, 17, out_type)) && tiles(256) >= 192) {
+    q.kernel = kTile256;
+    q.tile = 256;
+  } else if ((mean > 16 || kbytes <= 24 * kStep) && tiles(128) >= 512) {
+    q.kernel = kTile128;
+    q.tile = 128;
+  } else {
+    q.kernel = kTile64;
+    q.tile = 64;
+  }
+  q.tiles_n = (N - 1) / (gated ? q.tile / 2 : q.tile) + 1;
   q.row_tiles = (int64_t)(M - groups) / q.tile + groups;
   return q;
 }
