@@ -1011,6 +1011,13 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   };
   const int c = (int)(threadIdx.x % kPer) * 8;
   const int32_t n = n0 + c;
+  // Gathered: the rows of a once more, all together (they were not worth registers
+  // through the loop; loaded row by row here each would be waited for, 0.7 us a pass).
+  int32_t* s_rows = reinterpret_cast<int32_t*>(smem + kRows * kLd * 4);
+  if constexpr (kGroup) {
+    static_assert(kRows * kLd * 4 + kBM * 4 <= kSmem && kBM <= 64 * kWaves, "room for the rows");
+    if (p.index && threadIdx.x < kBM) s_rows[threadIdx.x] = m0 + threadIdx.x < p.M ? (int32_t)a_row_of(p, m0 + threadIdx.x) : -1;
+  }
   Columns<kKind, kGated, 8> cols;
   cols.load(p, n);
 #pragma unroll 1
@@ -1037,9 +1044,15 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
     for (int k = 0; k < kIters; ++k) {
       const int r = (int)threadIdx.x / kPer + k * kRowsPerIter;
       const int64_t m = m0 + tile_row(r, pass);
-      const int64_t ma = a_row_of(p, m < p.M ? m : (int64_t)p.M - 1);
-      const bool in = m < p.M && n < p.N && ma >= 0;
-      const int64_t mr = max(ma, (int64_t)0);
+      int64_t mr = m < p.M ? m : (int64_t)p.M - 1;
+      bool in = m < p.M && n < p.N;
+      if constexpr (kGroup) {
+        if (p.index) {
+          const int32_t ma = s_rows[tile_row(r, pass)];
+          in = ma >= 0 && n < p.N;
+          mr = max(ma, 0);
+        }
+      }
       float v[8], u[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
