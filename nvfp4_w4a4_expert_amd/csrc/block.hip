@@ -217,7 +217,7 @@ hipError_t launch(const BlockParams& p, hipStream_t stream) {
   auto go = [&](auto threads, auto vecs) {
     return launch_row_groups(block_kernel<kF16, kFp8, threads.value, vecs.value>, threads.value, p, stream);
   };
-  // Groups as the norm's but for rows of 2049 to 4096 elements: bound by the instructions
+  // Groups as the norm's but for rows between two groups of the norm: bound by the instructions
   // that it issues, and with two vectors a thread of 256 half a wavefront's are empty at 2816
   // (8192 rows: 256x2 43.9 us, 128x3 42.3, 512x1 54.9; 16 rows 4.8, 5.4, 4.2).
   if (nvec > 256 && nvec <= 512 && p.rows <= 512) return go(Count<512>{}, Count<1>{});

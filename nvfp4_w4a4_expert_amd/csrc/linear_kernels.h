@@ -118,8 +118,15 @@ __device__ __forceinline__ GroupTile group_tile(const GroupParams& p, int32_t bl
   int32_t q;
   group_place(block, all, p.tiles_n, q, t.tn);
   if (q < 0) return t;
-  const int32_t rest_upto = (int32_t)((int64_t)(q + 1) * (all - all_full) / all);
-  const bool is_full = rest_upto == (int32_t)((int64_t)q * (all - all_full) / all);
+  int32_t rest_upto, rest_before;
+  if (all < 46341) {                                           // (32-bit divisions are a quarter of the price)
+    rest_upto = (int32_t)((uint32_t)((q + 1) * (all - all_full)) / (uint32_t)all);
+    rest_before = (int32_t)((uint32_t)(q * (all - all_full)) / (uint32_t)all);
+  } else {
+    rest_upto = (int32_t)((int64_t)(q + 1) * (all - all_full) / all);
+    rest_before = (int32_t)((int64_t)q * (all - all_full) / all);
+  }
+  const bool is_full = rest_upto == rest_before;
   q = is_full ? q - rest_upto : rest_upto - 1;
   const int who = (int)__builtin_ctzll(__ballot((is_full ? upto_full : upto_rest) > q));  // the first prefix beyond q
   int32_t start = is_full ? upto_full - full : upto_rest - rest, e = -1, first = 0, end = 0, tm = 0;
@@ -968,7 +975,14 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   for (int ks = 0; ks < ring && ks < steps; ++ks) fetch(ks, ks * stage);
   if constexpr (kScaled)
     if (threadIdx.x < kBM + kBN) *reinterpret_cast<u32x4*>(s_scale[0][threadIdx.x]) = scale_words(load_scales(scale_row, 4 * step0, nblk));
-  step_barrier<0>();
+  // (grouped: short products count every microsecond before the first step)
+  if (kDeep && steps >= ring) {
+    if (ring == 2) step_barrier<kLoads>();
+    else if (ring == 3) step_barrier<2 * kLoads>();
+    else step_barrier<3 * kLoads>();
+  } else {
+    step_barrier<0>();
+  }
 #pragma unroll
   for (int j = 0; j < kFN; ++j) fw[j] = read_frag(smem + a_bytes + w_first * kStep, w_row(j) + i16, g);
   fa[0] = read_frag(smem + a_first * kStep, i16, g);
