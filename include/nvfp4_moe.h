@@ -739,8 +739,8 @@ typedef enum {
  *
  *   gain   device fp32 [1] (weight_scale_2) or NULL for 1.
  * Limits as for nvfp4_linear, with fp16 and NVFP4_W4_MX K <= 2^21; N' * K <= 2^36 and
- * M * K <= 2^34, N' the rows of w (else NVFP4_ERR_UNSUPPORTED).  The workspace holds w in
- * 16 bits where M is more than 64.
+ * M * K <= 2^34, N' the rows of w (else NVFP4_ERR_UNSUPPORTED).  The workspace (as for
+ * nvfp4_linear) holds sums of parts of K, or for many rows w in 16 bits.
  */
 NVFP4_API nvfp4_status_t nvfp4_linear_w4_workspace_size(const nvfp4_linear_t* p, int32_t w4,
                                                         size_t* bytes);

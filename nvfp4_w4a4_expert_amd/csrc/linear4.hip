@@ -508,6 +508,10 @@ Plan4 tile4_plan(const Linear4Args& a, int fm, int waves, int32_t slots, float s
   q.tiles_n = (a.N - 1) / (a.gated ? q.rows_w / 2 : q.rows_w) + 1;
   const int32_t steps = (a.K + 127) / 128;
   const int64_t total = (int64_t)q.tiles_m * q.tiles_n;
+  if (total > 0x7FFFFFFF / (64 * waves)) {                     // (threads of a launch; the largest tiles always fit)
+    q.cost = 3e38f;
+    return q;
+  }
   const int32_t left = (int32_t)(total % slots);
   const float rounds = (float)(total / slots) * (steps * step + rest);
   for (int32_t parts = 1; parts <= (left ? (slots / left < 16 ? slots / left : 16) : 1); ++parts) {

@@ -466,6 +466,7 @@ def quantize_fp4(w: torch.Tensor, scales: str = "nv", *, stream=None) -> FP4Rows
             scale = _empty_strided((1,), (1,), torch.float32)
             _lib.expert_absmax(w, ldw, K, None, 1, ends, 1, T, scale, handle)
             top = scale.item() / 2688.0
+            _need(top < float("inf"), "w must be finite")
             # (its reciprocal would leave fp32's range below 2^-126)
             scale.fill_(max(top, 2.0 ** -126) if top > 0 else 1.0)
             gscale = scale.reciprocal()
@@ -517,8 +518,8 @@ def linear(a: Operand, w: Union[Operand, FP4Rows], *, bias: Optional[torch.Tenso
     a [M, K] and w [N or 2N, K]: both bf16, both fp16, or both FP8Rows with the
     same kind of scales; K a multiple of 8 (16 for "row", 32 for "mx" operands).
     Or a in bf16 or fp16 and w as FP4Rows, K a multiple of 32 (nvfp4_linear_w4; all
-    products exact, "mx" weights in bf16's range; for more than 64 rows w is
-    written out in 16 bits, 2 * K bytes a row of memory for the call).
+    products exact, "mx" weights in bf16's range; for many rows w is written out
+    in 16 bits, 2 * K bytes a row of memory for the call).
     act: None, "silu", "gelu", "gelu_tanh" or "relu".  bias [N or 2N] and
     residual [M, N]: bf16, fp16 or fp32.  Returns [M, N] of `out_dtype` (a's
     type by default, bf16 for FP8Rows), or FP8Rows with "mx" scales for
