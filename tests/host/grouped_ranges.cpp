@@ -27,13 +27,9 @@ static void walk(const std::vector<int32_t>& sizes, int32_t N, bool gated, int k
   for (int32_t s : sizes) M += s;
   if (M == 0) return;
   const GroupPlan q = group_plan_of((int32_t)M, (int32_t)sizes.size(), N, 2816 * 2, kind, gated, out_type);
-  // tile rows: full ones of every group, then the groups' last ones
-  std::vector<std::pair<int32_t, int32_t>> rows;
-  for (size_t e = 0; e < sizes.size(); ++e)
-    for (int32_t t = 0; t < sizes[e] / q.tile; ++t) rows.push_back({(int32_t)e, t});
-  for (size_t e = 0; e < sizes.size(); ++e)
-    if (sizes[e] % q.tile) rows.push_back({(int32_t)e, sizes[e] / q.tile});
-  const int64_t used = (int64_t)rows.size(), total = used * q.tiles_n;
+  int64_t used = 0;                                            // tile rows of all groups
+  for (int32_t s : sizes) used += (s + q.tile - 1) / q.tile;
+  const int64_t total = used * q.tiles_n;
   need(used <= q.row_tiles, "the grid holds all row tiles", used, q.row_tiles);
   const int64_t blocks = group_blocks(q.row_tiles, q.tiles_n);
   need(blocks <= 0x7FFFFFFF && blocks >= total, "32-bit numbers", blocks);
