@@ -1113,17 +1113,27 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams p, int
   res.load(p, mr, n);
   float v[8] = {}, u[8] = {};
   const float* sum = p.partial + partial_at(left, 0, p.parts, r, c, bm, bn);
-  for (int32_t part = 0; part < p.parts; ++part, sum += (int64_t)bm * bn) {
+  // four parts' loads in flight, added in order
+  for (int32_t part = 0; part < p.parts; part += 4) {
+    f32x4 x[4][2], y[4][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sum + 4 * h);
-      const f32x4 y = *reinterpret_cast<const f32x4*>(sum + (kGated ? out_n : 0) + 4 * h);
+    for (int q = 0; q < 4; ++q) {
+      const float* from = sum + (int64_t)min(part + q, p.parts - 1) * bm * bn;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[4 * h + e] += x[e];
-        u[4 * h + e] += y[e];
+      for (int h = 0; h < 2; ++h) {
+        x[q][h] = *reinterpret_cast<const f32x4*>(from + 4 * h);
+        if constexpr (kGated) y[q][h] = *reinterpret_cast<const f32x4*>(from + out_n + 4 * h);
       }
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (part + q < p.parts) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] += x[q][i / 4][i % 4];
+          if constexpr (kGated) u[i] += y[q][i / 4][i % 4];
+        }
+      }
   }
   cols.finish(p, mr, v, u);
   res.add(p, v);

@@ -138,7 +138,7 @@ def test_every_code_and_scale_is_exact(M, dtype):
         ref = values(codes, sf)
         if form == "mx":
             # 2^127 times more than 1.5 is infinite in bf16; a NaN or infinity meets the zeros of a
-            ref = np.where(np.abs(ref) >= 2.0 ** 128, np.inf * np.sign(ref), ref)
+            ref = np.where(np.abs(ref) >= 2.0 ** 128, np.copysign(np.inf, ref), ref)
         ref = ref[:, np.arange(M) % K].T
         whole = np.isfinite(values(codes, sf)).all(1) & (np.abs(values(codes, sf)) < 2.0 ** 128).all(1)
         assert np.array_equal(got[:, whole], ref[:, whole]), form
