@@ -81,14 +81,6 @@ __device__ __forceinline__ f32x4 mma4(const u32x4& w, const u32x4& a, f32x4 acc)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), __builtin_bit_cast(bf16x8_t, a), acc, 0, 0, 0);
 }
 
-// ---- few rows -------------------------------------------------------------------
-// A workgroup owns 16 * kFN rows of w (gated: gate rows, then up rows) and 16 * kRF rows
-// of a.  Its wavefronts take groups of 128 elements of K in turn, kBatch groups' loads in
-// flight at once and the next ones' w on its way: a lane's 16 bytes of w are 32 elements
-// of a row, the next 32 belong to the next group of 16 lanes, and the four matrix
-// instructions of a group take 8 elements of each (any order of K that both operands
-// share).  The wavefronts' sums are added in order through LDS, 16 rows at a time.
-//
 // The block scales of 128 elements of a row, `blocks` of them inside it (a multiple of 32
 // elements): 8 bytes of E4M3 at an even address, or 4 of UE8M0 at any.  Those past the
 // end are zeros.
@@ -106,6 +98,16 @@ __device__ __forceinline__ void load_scales4(const uint8_t* at, int32_t blocks, 
     if (i < blocks) s[i / 4] |= (uint32_t)at[i] << (8 * (i % 4));
 }
 
+// ---- few rows -------------------------------------------------------------------
+// A workgroup owns 16 * kFN rows of w (gated: gate rows, then up rows) and 16 * kRF rows
+// of a.  Its wavefronts take groups of 128 elements of K in turn, kBatch groups' loads in
+// flight at once and the next ones' w on its way: a lane's 16 bytes of w are 32 elements
+// of a row, the next 32 belong to the next group of 16 lanes, and the four matrix
+// instructions of a group take 8 elements of each (any order of K that both operands
+// share).  The wavefronts' sums are added in order through LDS, 16 rows at a time.
+// One row of 2 x 2112 x 2816 takes 6.6 us (6.7 MB: a launch, two rounds of loads and the
+// join in LDS), of 8192 x 8192 17 with E4M3 scales and 15 with UE8M0 (37.7 and 35.7 MB, 2.3
+// TB/s: with 16 wavefronts a CU their turns of load and widening leave the memory idle).
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
 __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
   constexpr int kWaves = 8, kRows = 16 * kFN, kCols = kGated ? kRows / 2 : kRows;
@@ -248,12 +250,14 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
 
 // ---- middle numbers of rows -----------------------------------------------------------
 // A workgroup of four wavefronts owns kBM = 16 kFM rows of a and 128 rows of w (gated: 64
-// gate rows and their up rows), each wavefront 32 of the latter, and all or a part of
-// K.  Reading w once would cost less than reading a again for every few rows of w (M = 64,
-// 8192 x 8192: 268 MB from L2 in the form above), so both go to LDS, 128 elements of K a
-// step and w as codes; a wavefront widens its own rows of w, once for all rows of a.  Lane
-// group g holds elements 32 g .. 32 g + 31 of a step, the t-th matrix instruction takes
-// eight of them.
+// gate rows and their up rows), of eight 128 rows of a and 256 of w, each wavefront 32 of
+// the latter, and all or a part of K.  The form above reads a again for every few rows of w
+// (64 x 8192 x 8192: 268 MB from L2, 41 us for 27 here), so both go to LDS, 128 elements of
+// K a step and w as codes; a wavefront widens its own rows of w, once for all rows of a.
+// Lane group g holds elements 32 g .. 32 g + 31 of a step, the t-th matrix instruction
+// takes eight of them.  16 x 8192 x 8192 takes 11.9 us with UE8M0 scales and 5 for joining
+// eight parts (35.7 MB, 3 TB/s while it runs); from 64 rows on the widening bounds it, which
+// more rows a tile share.
 template <int kFM, int kWaves>
 struct TileOf {
   static constexpr int kBM = 16 * kFM, kRowsW = 32 * kWaves, kThreads = 64 * kWaves;
