@@ -280,27 +280,29 @@ _GATE_ACTS = {None: _lib.GATE_PLAIN, "none": _lib.GATE_PLAIN, "sigmoid": _lib.GA
 
 def _gate(gate, T, K, dtype):
     """(address, row stride, columns, type) of a gate tensor that broadcasts to [T, K]."""
-    if gate.layout is not torch.strided or gate.dtype not in (dtype, torch.float32) or \
-            gate.dim() not in (1, 2) or gate.shape[-1] not in (1, K) or \
-            (gate.dim() == 2 and gate.shape[0] not in (1, T)):
+    shape = gate.shape
+    n = len(shape)
+    cols = shape[-1] if n else 0
+    if not (gate.layout is torch.strided and (gate.dtype is dtype or gate.dtype is torch.float32) and
+            (cols == 1 or cols == K) and (n == 1 or (n == 2 and shape[0] in (1, T)))):
         raise ValueError(f"gate must be a number or a {dtype} or fp32 tensor of [1], [{K}], [1, {K}], "
                          f"[{T}, 1] or [{T}, {K}]")
-    st = gate.stride()
-    ld = st[0] if gate.dim() == 2 and gate.shape[0] == T and T > 1 else 0
-    wide = gate.shape[-1] == K
-    if wide and T and (st[-1] != 1 or gate.data_ptr() % 16 or ld * gate.element_size() % 16 or 0 < ld < K):
+    ld = gate.stride(0) if n == 2 and shape[0] == T and T > 1 else 0
+    at = gate.data_ptr()
+    if cols == K and T and (gate.stride(-1) != 1 or at % 16 or ld * gate.element_size() % 16 or 0 < ld < K):
         raise ValueError("gate's rows must be contiguous and start on 16-byte boundaries")
-    return gate.data_ptr(), ld, K if wide else 1, _TYPES[gate.dtype]
+    return at, ld, cols, _TYPES[gate.dtype]
 
 
 def _weight(w, name, K, dtype):
-    """The address of a norm's weight, checked."""
+    """The address of a norm's weight (0 without one), checked."""
     if w is None:
-        return None
-    if not (isinstance(w, torch.Tensor) and w.dtype == dtype and w.shape == (K,) and
-            w.is_contiguous() and w.data_ptr() % 16 == 0):
-        raise ValueError(f"{name} must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
-    return w.data_ptr()
+        return 0
+    if isinstance(w, torch.Tensor) and w.dtype is dtype and w.shape == (K,) and w.is_contiguous():
+        at = w.data_ptr()
+        if not at % 16:
+            return at
+    raise ValueError(f"{name} must be a contiguous 16-byte aligned {dtype} [{K}] tensor")
 
 
 def block_norm(x: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = True,
@@ -339,7 +341,8 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = Tru
         act = _GATE_ACTS[gate_act]
     except (KeyError, TypeError):
         raise ValueError(f"gate_act must be one of {[k for k in _GATE_ACTS]}, not {gate_act!r}") from None
-    g_at, ldg, gate_cols, gate_type, gate_scale = None, 0, 0, 0, 1.0
+    g_at = ldg = gate_cols = gate_type = 0
+    gate_scale = 1.0
     gate_t = gate if isinstance(gate, torch.Tensor) else None
     if gate_t is not None:
         g_at, ldg, gate_cols, gate_type = _gate(gate, T, K, dtype)
@@ -356,7 +359,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = Tru
     if not (0.0 <= eps < 3.4e38 and -3.4e38 < weight_offset < 3.4e38 and
             -3.4e38 < gate_scale < 3.4e38 and -3.4e38 < residual_scale < 3.4e38):
         raise ValueError("eps must be finite and >= 0, weight_offset, gate and residual_scale finite")
-    y_at = codes_at = scales_at = None
+    y_at = codes_at = scales_at = 0
     ldy = ldt = K
     if out is not None:
         _need(want_y, "out needs want_y")
@@ -380,7 +383,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = Tru
             kind = _FP8[scales]
             fp8 = _fp8_out(T, K, scales)
             codes_at, scales_at = fp8.codes.data_ptr(), fp8.scales.data_ptr()
-        _lib.block_norm(_lib.BlockNorm(
+        _lib.block_norm(_lib.pack_block_norm(
             x_at, r_at, p_at, w_at, g_at, t_at, y_at, codes_at, scales_at, ldx, ldr, ldg, ldt, ldy,
             T, K, _TYPES[dtype], post_norm, gate_type, gate_cols, act, kind,
             weight_offset, eps, gate_scale, residual_scale), handle)

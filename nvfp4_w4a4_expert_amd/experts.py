@@ -40,11 +40,13 @@ class Grouping(NamedTuple):
 
 def _vector(t, name, dtype, shape):
     """The address of a contiguous tensor of one of the shapes, checked."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.layout is torch.strided and
-            tuple(t.shape) in shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {str(dtype).replace('torch.', '')} "
-                         f"{' or '.join(str(list(s)) for s in shape)} tensor")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.layout is torch.strided and t.is_contiguous():
+        have = t.shape
+        for s in shape:
+            if have == s:
+                return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {str(dtype).replace('torch.', '')} "
+                     f"{' or '.join(str(list(s)) for s in shape)} tensor")
 
 
 def route(logits: torch.Tensor, k: int, *, stream=None) -> Routing:
@@ -150,14 +152,14 @@ def grouped_linear(a: Operand, w: Operand, offsets: torch.Tensor, *, index: Opti
     except (KeyError, TypeError):
         raise ValueError(f"act must be one of {[k for k in _ACTS]}, not {act!r}") from None
     offsets_at = _vector(offsets, "offsets", torch.int32, ((E + 1,),))
-    P, index_at = T, None
+    P, index_at = T, 0
     if index is not None:
         _need(isinstance(index, torch.Tensor) and index.dim() == 1, "index must be an int32 [rows] tensor")
         P = index.shape[0]
         index_at = _vector(index, "index", torch.int32, ((P,),))
     if not (isinstance(index_div, int) and 1 <= index_div <= 0x7FFFFFFF):
         raise ValueError("index_div must be a positive integer")
-    bias_type, bias_at = 0, None
+    bias_type = bias_at = 0
     if bias is not None:
         _need(isinstance(bias, torch.Tensor) and bias.dtype in _FLOATS, "bias must be a bf16, fp16 or fp32 tensor")
         bias_at, bias_type = _vector(bias, "bias", bias.dtype, ((E, rows),)), _TYPES[bias.dtype]
@@ -186,9 +188,9 @@ def grouped_linear(a: Operand, w: Operand, offsets: torch.Tensor, *, index: Opti
             res, out_scales = _fp8_out(P, N, "mx")
         else:
             res = _empty(P, N, out_dtype) if out is None else out
-        _lib.grouped_linear(_lib.GroupedLinear(
-            a_at, a_sc_at, wv.data_ptr(), None if w_sc is None else w_sc.data_ptr(), bias_at, offsets_at,
-            index_at, res.data_ptr(), None if out_scales is None else out_scales.data_ptr(), lda, ldw, each,
+        _lib.grouped_linear(_lib.pack_grouped_linear(
+            a_at, a_sc_at or 0, wv.data_ptr(), 0 if w_sc is None else w_sc.data_ptr(), bias_at, offsets_at,
+            index_at, res.data_ptr(), 0 if out_scales is None else out_scales.data_ptr(), lda, ldw, each,
             ldo, P, T, E, N, K, index_div, kind, bias_type, out_type, act_id, gated), handle)
     return FP8Rows(res, out_scales) if mx else res
 

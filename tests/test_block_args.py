@@ -97,3 +97,13 @@ def test_c_entry_limits_and_empty_calls():
     assert L._lib.nvfp4_block_norm(None, None) == L.ERR_INVALID_ARG
     assert L._lib.nvfp4_block_norm(ctypes.byref(fields(K=32776, ldx=32776, ldr=32776, ldt=32776, ldy=32776)), None) == L.ERR_UNSUPPORTED
     assert L._lib.nvfp4_block_norm(ctypes.byref(fields(num_rows=0, x=None, residual=None)), None) == L.OK
+
+
+def test_packed_fields_are_the_structures():
+    """The byte forms of the calls hold every field where the structure has it."""
+    for cls, pack in ((L.BlockNorm, L.pack_block_norm), (L.GroupedLinear, L.pack_grouped_linear)):
+        values = [(i + 1) * 3 if t is not ctypes.c_float else i + 0.5 for i, (_, t) in enumerate(cls._fields_)]
+        data = pack(*values)
+        assert len(data) == ctypes.sizeof(cls)
+        got = cls.from_buffer_copy(data)
+        assert [getattr(got, name) for name, _ in cls._fields_] == values
