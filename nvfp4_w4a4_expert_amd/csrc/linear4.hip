@@ -523,7 +523,7 @@ Plan4 tile4_plan(const Linear4Args& a, int fm, int waves, int32_t slots, float s
     if ((steps + each - 1) / each != parts) continue;
     float cost = rounds;
     if (left) cost += each * step + rest;
-    if (parts > 1) cost += 3.0f + (float)left * parts * q.bm * q.rows_w * 8.0f / 4e6f;
+    if (parts > 1) cost += 3.0f + (float)left * parts * q.bm * q.rows_w * 8.0f / 8e6f;
     if (q.cost == 0 || cost < q.cost) {
       q.cost = cost;
       q.parts = parts;
@@ -544,6 +544,11 @@ Plan4 tile4_plan(const Linear4Args& a, int fm, int waves, int32_t slots, float s
 // 26, 20, 21, 28, 47, 81; 64 rows -, 38, 27, 28, 46, 80; 256 rows -, 119, 66, 58, 51, 118;
 // 1024 rows -, 448, 245, 184, 141, 174.  4096 x (2 x 2112) x 2816: 64-row tiles 142, 128-row
 // tiles 130, written out 114.
+// Sums of parts pass at 8 MB/us (written and read once, mostly in the last-level cache).  At
+// half that rate and 7 us beside the steps of the 16- and 32-row tiles, against 8 and 4:
+// 8192 x 8192 in bf16 58.4 and 51.9 for 256 rows, 96.0 and 84.4 for 512; 512 x (2 x 2112) x
+// 2816 34.7 and 33.2; 16 rows with UE8M0 16.4 and 15.6; but 256 x 1411 x 2112 with UE8M0
+// 12.0 and 14.2, 512 x 1411 x 2112 20.2 and 21.2, 300 x 8192 x 8192 with UE8M0 69.6 and 71.4.
 Plan4 plan4_of(const Linear4Args& a) {
   Plan4 few = {}, wide = {};
   few.form = Plan4::kFew;
@@ -552,11 +557,11 @@ Plan4 plan4_of(const Linear4Args& a) {
   const float rows = a.gated ? 2.0f * a.N : (float)a.N, weights = rows * a.K;
   const int c = a.mx ? 2 : a.kind == kF16 ? 1 : 0;
   static const float kStepUs[4][3] = {{0.9f, 0.76f, 0.58f}, {0.95f, 0.8f, 0.74f}, {1.38f, 1.27f, 1.08f}, {2.1f, 2.0f, 1.87f}};
-  Plan4 best = tile4_plan(a, 1, 4, 512, kStepUs[0][c], 7.0f);
+  Plan4 best = tile4_plan(a, 1, 4, 512, kStepUs[0][c], 4.0f);
   auto take = [&](const Plan4& q) {
     if (q.cost < best.cost) best = q;
   };
-  if (a.M > 16) take(tile4_plan(a, 2, 4, 512, kStepUs[1][c], 7.0f));
+  if (a.M > 16) take(tile4_plan(a, 2, 4, 512, kStepUs[1][c], 4.0f));
   if (a.M > 32) take(tile4_plan(a, 4, 4, 512, kStepUs[2][c], 6.0f));
   if (a.M > 64) take(tile4_plan(a, 8, 8, 256, kStepUs[3][c], 10.0f));
   if (a.M <= 16) {
