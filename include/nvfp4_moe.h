@@ -763,8 +763,8 @@ NVFP4_API nvfp4_status_t nvfp4_linear_w4(const nvfp4_linear_t* p, int32_t w4, co
  * [offsets[0], offsets[num_experts]) are not written, nor those whose index is outside
  * [0, a_rows * index_div).  An offset counts as the largest of those up to it, held in
  * [0, num_rows]: offsets out of order or range leave groups empty and lead nowhere else.
- * Accumulation, rounding and types as for nvfp4_linear; 8-bit operands with a 16-bit
- * output may take the scaled instruction whatever the number of rows.
+ * Accumulation, rounding and types as for nvfp4_linear with at most 16 rows: products of
+ * 8-bit operands are exact whatever the output's type and the number of rows.
  *
  *   a            device [a_rows, lda] of `type`; a_rows >= num_rows without an index.
  *   w            device [num_experts, N or 2N, ldw], w_each elements from one expert to

@@ -8,7 +8,8 @@
 // with the start of the kernel, by prefixes over the experts in every wavefront), those
 // without a tile end.  A tile belongs to one expert, so a group's last tile is partly
 // empty: it leaves out the instructions, copies and epilogue of its empty rows and keeps
-// more steps on their way.  Rows of a are gathered by the copies into LDS themselves.
+// more steps on their way (16-bit operands; 8-bit ones are converted to bf16, so that their
+// products are exact).  Rows of a are gathered by the copies into LDS themselves.
 #include "internal.h"
 #include "linear_kernels.h"
 
@@ -72,11 +73,9 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {
   p.bias_each = rows;
   p.experts = a.experts; p.a_rows = a.a_rows; p.index_div = a.index_div;
   const GroupPlan plan = plan_for(a);
-  switch (kind_of(a.kind, 17, a.out_type)) {
+  switch (kind_of(a.kind, 1, a.out_type)) {                    // exact products at any number of rows (group_plan_of)
     case kBf16: return go_gated<kBf16>(p, a.gated, plan, stream);
     case kF16: return go_gated<kF16>(p, a.gated, plan, stream);
-    case kRow8: return go_gated<kRow8>(p, a.gated, plan, stream);
-    case kBlock8: return go_gated<kBlock8>(p, a.gated, plan, stream);
     case kRow8Wide: return go_gated<kRow8Wide>(p, a.gated, plan, stream);
     case kBlock8Wide: return go_gated<kBlock8Wide>(p, a.gated, plan, stream);
   }

@@ -648,7 +648,8 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
   // Grouped: a group's last tile has few rows of a to keep, and w for it comes from memory,
   // so its steps get as many buffers as LDS holds (two workgroups of 128-row tiles a CU).
   constexpr bool kDeep = kGroup && kBM >= 128 && !is_wide(kKind);
-  constexpr int kSmem = !kDeep ? kStages * kStage : kBM == 256 ? 160 * 1024 - (kScaled ? 2 * (kBM + kBN) * 16 : 0) : 72 * 1024;
+  static_assert(!kDeep || !kScaled, "scales would take a part of the LDS");
+  constexpr int kSmem = !kDeep ? kStages * kStage : kBM == 256 ? 160 * 1024 : 72 * 1024;
   __shared__ __align__(1024) char smem[kSmem];
   __shared__ __align__(16) uint32_t s_scale[kScaled ? 2 : 1][kScaled ? kBM + kBN : 1][4];
 
@@ -713,7 +714,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void linear_tile_kernel(const Pa
       const bool quarter = kBM == 256 && rows <= kBM / 4;
       a_bytes = (quarter ? kBM / 4 : kBM / 2) * kStep;
       stage = a_bytes + kBN * kStep;
-      ring = quarter && !kScaled ? 4 : 3;
+      ring = quarter ? 4 : 3;
     }
   }
   // (a wavefront copies all rows of its part or, behind the last row, none: step_barrier

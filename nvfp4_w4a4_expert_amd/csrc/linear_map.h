@@ -119,8 +119,15 @@ inline int kind_of(int kind, int32_t M, int32_t out_type) {
 // a router with likes, 128 experts, hidden 2816, intermediate 704, top-8: gate/up in bf16 of
 // 1 token 18 / 32 / -, 4: 28 / 45 / -, 16: 56 / 56 / -, 64: 75 / 86 / -, 256: 113 / 119 / -,
 // 512: 150 / 129 / 163, 1024: 219 / 181 / 200, 2048: 359 / 271 / 265, 4096: 615 / 393 / 382;
-// with block scales 16: 42 / 35 / -, 256: 90 / 76 / -, 4096: 493 / 252 / 236; down in bf16 of
-// 16: 40 / 33 / -, 256: 79 / 67 / -.  8 experts, top-2, 333 x 1411 x 704 fp16 12.5 / 17 / 36.
+// with block scales 1: 20 / 30, 16: 49 / 49, 256: 103 / 95, 4096: 546 / 344; down in bf16 of
+// 16: 40 / 33 / -, 256: 79 / 67 / -, with block scales 1: 13 / 15, 16: 42 / 33, 4096: 478 / 253.
+// 8 experts, top-2, 333 x 1411 x 704 fp16 12.5 / 17 / 36.
+//
+// 8-bit operands have exact products whatever the result's type and the number of rows, as
+// the linear operator's of at most 16 rows: groups often hold a few, and a row would have
+// other bits in another batch.  The scaled instruction, which cuts products (linear.hip),
+// took 34 us in place of 50 for gate/up of 16 tokens with block scales, 247 in place of 342
+// for 4096 and 208 in place of 254 for down of 4096.
 struct GroupPlan {
   int kernel;
   int32_t tile, tiles_n;
@@ -135,7 +142,7 @@ inline GroupPlan group_plan_of(int32_t M, int32_t experts, int32_t N, int32_t kb
     return (rows > groups ? rows : groups) * ((N - 1) / (gated ? tile / 2 : tile) + 1);
   };
   GroupPlan q;
-  if (mean >= 128 && !is_wide(kind_of(kind, 17, out_type)) && tiles(256) >= 192) {
+  if (mean >= 128 && !is_wide(kind_of(kind, 1, out_type)) && tiles(256) >= 192) {
     q.kernel = kTile256;
     q.tile = 256;
   } else if ((mean > 16 || kbytes <= 24 * kStep) && tiles(128) >= 512) {

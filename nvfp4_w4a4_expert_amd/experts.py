@@ -135,9 +135,7 @@ def grouped_linear(a: Operand, w: Operand, offsets: torch.Tensor, *, index: Opti
     int32 [experts + 1]; bias [experts, N or 2N] bf16, fp16 or fp32.  Returns
     [rows, N] of `out_dtype` (a's type by default, bf16 for FP8Rows), or FP8Rows
     with "mx" scales for "mx" (N a multiple of 32).  `out` receives the result.
-
-    FP8Rows with a 16-bit result may run on the scaled matrix instruction, as
-    dense.linear says for more than 16 rows."""
+    Products are exact and sums fp32, of FP8Rows too."""
     kind, T, K, lda, a_at, av, a_sc, a_sc_at = _operand(a, "a")
     E, rows, wK, ldw, each, wv, w_sc = _expert_weights(w, kind, "a")
     if wK != K:
