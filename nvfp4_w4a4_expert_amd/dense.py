@@ -454,13 +454,15 @@ def quantize_fp4(w: torch.Tensor, scales: str = "nv", *, stream=None) -> FP4Rows
     """bf16 weights [rows, K] -> FP4Rows, at load time: "nv" scales with the fp32
     scale max|w| / 2688 (1 for a matrix of zeros), or "mx" scales alone.  K is a
     multiple of 32.  The quantiser is the experts' own (nvfp4_quantize_experts and its
-    UE8M0 form, the matrix as one expert); "nv" waits for the matrix's maximum."""
+    UE8M0 form, the matrix as one expert).  Waits for the check that w is finite: the
+    codes have no NaN or infinity."""
     T, K, ldw, _ = _rows(w, "w", None, None, (torch.bfloat16,))
     if not (isinstance(scales, str) and scales in ("nv", "mx")):
         raise ValueError('scales must be "nv" or "mx"')
     _need(K >= 32 and K % 32 == 0, f"w must have a multiple of 32 columns, not {K}")
     handle, ctx = _on((w,), stream)
     with ctx:
+        _need(bool(torch.isfinite(w).all()), "w must be finite")
         nv = scales == "nv"
         codes, sf = _empty(T, K // 2, torch.uint8), _empty(T, K // (16 if nv else 32), torch.uint8)
         ends = torch.tensor([0, T], dtype=torch.int32, device=w.device)
@@ -469,7 +471,6 @@ def quantize_fp4(w: torch.Tensor, scales: str = "nv", *, stream=None) -> FP4Rows
             scale = _empty_strided((1,), (1,), torch.float32)
             _lib.expert_absmax(w, ldw, K, None, 1, ends, 1, T, scale, handle)
             top = scale.item() / 2688.0
-            _need(top < float("inf"), "w must be finite")
             # (its reciprocal would leave fp32's range below 2^-126)
             scale.fill_(max(top, 2.0 ** -126) if top > 0 else 1.0)
             gscale = scale.reciprocal()
