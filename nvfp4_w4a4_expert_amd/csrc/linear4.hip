@@ -72,6 +72,19 @@ __device__ __forceinline__ void split_f16(const u32x4& a, u32x4& hi, u32x4& lo) 
   }
 }
 
+// bf16 weights without their infinities, which the upper part of an fp16 number has met
+// already: 0 for a lower part of 0, infinity times 0 would be NaN.  Elements are infinite
+// from scale code 253 on.
+constexpr uint32_t kInfiniteFrom = 253;
+__device__ __forceinline__ u32x4 finite_bf16(u32x4 w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+  }
+  return w;
+}
+
 // acc += w . a over 32 elements of K, w the row operand
 template <bool kMx, bool kHalf>
 __device__ __forceinline__ f32x4 mma4(const u32x4& w, const u32x4& a, f32x4 acc) {
@@ -182,7 +195,7 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      auto part = [&](auto tc) {
+      auto part = [&](auto tc, auto infinite) {
         constexpr int t = decltype(tc)::value;
         u32x4 wt[kFN];
 #pragma unroll
@@ -195,17 +208,29 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = mma4<kMx, kHalf>(wt[j], hi, acc[i][j]);
 #pragma unroll
-            for (int j = 0; j < kFN; ++j) acc[i][j] = mma4<kMx, kHalf>(wt[j], lo, acc[i][j]);
+            for (int j = 0; j < kFN; ++j) acc[i][j] = mma4<kMx, kHalf>(infinite.value ? finite_bf16(wt[j]) : wt[j], lo, acc[i][j]);
           } else {
 #pragma unroll
             for (int j = 0; j < kFN; ++j) acc[i][j] = mma4<kMx, kHalf>(wt[j], a[b][i][t], acc[i][j]);
           }
         }
       };
-      part(std::integral_constant<int, 0>{});
-      part(std::integral_constant<int, 1>{});
-      part(std::integral_constant<int, 2>{});
-      part(std::integral_constant<int, 3>{});
+      auto group = [&](auto infinite) {
+        part(std::integral_constant<int, 0>{}, infinite);
+        part(std::integral_constant<int, 1>{}, infinite);
+        part(std::integral_constant<int, 2>{}, infinite);
+        part(std::integral_constant<int, 3>{}, infinite);
+      };
+      if constexpr (kSplit) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) top = max(top, now.s[b][j]);
+        if (__any(top >= kInfiniteFrom)) {                     // (for the whole wavefront)
+          group(std::true_type{});
+          continue;
+        }
+      }
+      group(std::false_type{});
     }
     now = next;
   }
@@ -447,7 +472,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void linear4_tile_kernel(const LinP
 }
 
 // ---- many rows ------------------------------------------------------------------------
-// w in 16 bits, dense rows of `copies` times K elements; a thread writes 32 elements.
+// w in 16 bits, dense rows of `copies` times K elements, the second copy (for the lower
+// parts of a) without its infinities; a thread writes 32 elements.
 template <bool kMx, bool kHalf>
 __global__ __launch_bounds__(256) void widen4_kernel(const uint8_t* w, int64_t ldw, const uint8_t* scales, int64_t rows, int32_t K,
                                                      int32_t copies, uint16_t* out) {
@@ -472,7 +498,7 @@ __global__ __launch_bounds__(256) void widen4_kernel(const uint8_t* w, int64_t l
   for (int32_t i = 0; i < copies; ++i) {
     u32x4* dst = reinterpret_cast<u32x4*>(out + (row * copies + i) * K + 32 * v);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) dst[t] = d[t];
+    for (int t = 0; t < 4; ++t) dst[t] = i ? finite_bf16(d[t]) : d[t];
   }
 }
 
