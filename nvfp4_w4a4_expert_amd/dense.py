@@ -43,8 +43,8 @@ _ACTS = {None: _lib.ACT_NONE, "none": _lib.ACT_NONE, "silu": _lib.ACT_SILU,
 
 class FP8Rows(NamedTuple):
     """Rows held in 8 bits: E4M3 codes uint8 [rows, K] and their scales, fp32
-    [rows] ("row") or UE8M0 uint8 [rows, K/32] ("mx").  Where an FP8Rows is
-    taken, any (codes, scales) pair is."""
+    [rows] ("row") or UE8M0 uint8 [rows, K/32] ("mx"); experts' weights with the
+    experts first in both.  Where an FP8Rows is taken, any (codes, scales) pair is."""
     codes: torch.Tensor
     scales: torch.Tensor
 
@@ -52,7 +52,7 @@ class FP8Rows(NamedTuple):
         """The values, in fp32 (with torch operations)."""
         v = self.codes.view(torch.float8_e4m3fn).float()
         if self.scales.dtype == torch.float32:
-            return v * self.scales[:, None]
+            return v * self.scales[..., None]
         s = self.scales.view(torch.float8_e8m0fnu).float()
         return (v.view(*s.shape, 32) * s[..., None]).view(v.shape)
 
