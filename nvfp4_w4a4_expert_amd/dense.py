@@ -69,12 +69,12 @@ class FP4Rows(NamedTuple):
     def dequantize(self) -> torch.Tensor:
         """The values, in fp32 (with torch operations)."""
         table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=self.codes.device)
-        c = torch.stack([self.codes & 15, self.codes >> 4], 2).view(self.codes.shape[0], -1).int()
+        c = torch.stack([self.codes & 15, self.codes >> 4], 2).flatten(1).int()
         v = torch.where(c >= 8, -table[c & 7], table[c & 7])
         mx = self.codes.shape[1] * 2 == self.scales.shape[1] * 32
         s = self.scales.view(torch.float8_e8m0fnu if mx else torch.float8_e4m3fn).float()
         v = (v.view(*s.shape, 32 if mx else 16) * s[..., None]).view(v.shape)
-        return v if self.scale is None else v * self.scale
+        return v if self.scale is None else v * self.scale.reshape(())
 
 
 class NormOut(NamedTuple):
