@@ -179,6 +179,7 @@ def grouped_linear(a: Operand, w: Operand, offsets: torch.Tensor, *, index: Opti
             ldo = _plain(out, "out", (P, N), (out_dtype,))
             _check_apart(out, "out", (av, wv, a_sc, w_sc, bias, offsets, index))
     _lib._check_size(P, "rows of the result")
+    _lib._check_size(rows, "rows of w")
     handle, ctx = _on((av, wv, a_sc, w_sc, bias, offsets, index, out), stream)
     with ctx:
         out_scales = None
