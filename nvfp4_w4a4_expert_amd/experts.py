@@ -19,7 +19,7 @@ from typing import NamedTuple, Optional, Union
 import torch
 
 from . import _lib
-from .dense import (_ACTS, _FLOATS, _TYPES, FP8Rows, Operand, _check_apart, _empty, _empty_strided, _fp8_out, _need, _on,
+from .dense import (_ACTS, _FLOATS, _HALF, _TYPES, FP8Rows, Operand, _check_apart, _empty, _empty_strided, _fp8_out, _need, _on,
                     _operand, _plain, _rows, quantize_fp8)
 
 
@@ -86,20 +86,20 @@ def permute(ids: torch.Tensor, num_experts: int, *, stream=None) -> Grouping:
     return out
 
 
-def _expert_weights(w, kind, a_name):
+def _expert_weights(w, kind, like, name="w"):
     """(experts, rows, K, row stride, expert stride, values, scales) of a grouped
-    product's weights, checked; kind is a's."""
+    product's weights, checked; kind is that of `like`, the operand beside them."""
     scales = None
     if kind in (_lib.TYPE_FP8_ROW, _lib.TYPE_FP8_MX):
-        _need(isinstance(w, tuple) and len(w) == 2, f"w must be an FP8Rows, as {a_name}")
+        _need(isinstance(w, tuple) and len(w) == 2, f"{name} must be an FP8Rows, as {like}")
         w, scales = w
         dtype = torch.uint8
     else:
         dtype = torch.bfloat16 if kind == _lib.TYPE_BF16 else torch.float16
     _need(isinstance(w, torch.Tensor) and w.dtype == dtype and w.dim() == 3 and w.layout is torch.strided,
-          f"w must be a {str(dtype).replace('torch.', '')} [experts, rows, K] tensor, as {a_name}")
+          f"{name} must be a {str(dtype).replace('torch.', '')} [experts, rows, K] tensor, as {like}")
     E, rows, K = w.shape
-    _need(1 <= E <= 1024, f"w must hold between 1 and 1024 experts, not {E}")
+    _need(1 <= E <= 1024, f"{name} must hold between 1 and 1024 experts, not {E}")
     per16 = 16 // w.element_size()
     each, ld, step = w.stride()
     if rows <= 1:
@@ -108,10 +108,10 @@ def _expert_weights(w, kind, a_name):
         each = 0
     if rows and K and ((step != 1 and K != 1) or ld < K or ld % per16 or each % per16 or w.data_ptr() % 16 or
                        (E > 1 and each < (rows - 1) * ld + K)):
-        raise ValueError("w's rows must be contiguous, apart and start on 16-byte boundaries")
+        raise ValueError(f"{name}'s rows must be contiguous, apart and start on 16-byte boundaries")
     if scales is not None:
         shape, dtype = ((E, rows), torch.float32) if kind == _lib.TYPE_FP8_ROW else ((E, rows, K // 32), torch.uint8)
-        _vector(scales, "w's scales", dtype, (shape,))
+        _vector(scales, f"{name}'s scales", dtype, (shape,))
     return E, rows, K, ld, each, w, scales
 
 
@@ -241,16 +241,31 @@ class ExpertsLayer:
 
     def __init__(self, w13: Operand, w2: Operand, *, act: str = "silu", bias13: Optional[torch.Tensor] = None,
                  bias2: Optional[torch.Tensor] = None):
+        if isinstance(w13, tuple) and len(w13) == 2 and isinstance(w13[1], torch.Tensor):
+            kind, step = (_lib.TYPE_FP8_ROW, 16) if w13[1].dtype == torch.float32 else (_lib.TYPE_FP8_MX, 32)
+        else:
+            _need(isinstance(w13, torch.Tensor) and w13.dtype in _HALF, "w13 must be a bf16 or fp16 tensor or an FP8Rows")
+            kind, step = _TYPES[w13.dtype], 8
+        E, rows, H = _expert_weights(w13, kind, "w13", "w13")[:3]
+        E2, H2, inter = _expert_weights(w2, kind, "w13", "w2")[:3]
+        _need(rows == 2 * inter and E2 == E and H2 == H,
+              f"w13 [{E}, {rows}, {H}] must be [experts, 2 * inter, hidden] and w2 [{E2}, {H2}, {inter}] [experts, hidden, inter]")
+        _need(H >= step and inter >= step and H % step == 0 and inter % step == 0,
+              f"hidden and inter must be multiples of {step}, not {H} and {inter}")
+        for b, name, n in ((bias13, "bias13", rows), (bias2, "bias2", H)):
+            if b is not None:
+                _need(isinstance(b, torch.Tensor) and b.dtype in _FLOATS, f"{name} must be a bf16, fp16 or fp32 tensor")
+                _vector(b, name, b.dtype, ((E, n),))
+        _need(act is None or isinstance(act, str) and act in _ACTS, f"act must be one of {[k for k in _ACTS]}, not {act!r}")
         self.w13, self.w2, self.act, self.bias13, self.bias2 = w13, w2, act, bias13, bias2
-        self.scales = None
-        if isinstance(w13, tuple):
-            self.scales = "row" if w13[1].dtype == torch.float32 else "mx"
-        self.num_experts = (w13 if self.scales is None else w13[0]).shape[0]
+        self.scales = {_lib.TYPE_FP8_ROW: "row", _lib.TYPE_FP8_MX: "mx"}.get(kind)
+        self.num_experts = E
 
     @classmethod
     def quantized(cls, w13: torch.Tensor, w2: torch.Tensor, scales: str = "mx", **kw) -> "ExpertsLayer":
         """The layer in 8 bits, from bf16 or fp16 weights."""
         def fp8(w):
+            _need(isinstance(w, torch.Tensor) and w.dim() == 3, "w13 and w2 must be [experts, rows, K] tensors")
             q = quantize_fp8(w.reshape(-1, w.shape[2]), scales)
             return FP8Rows(*(t.view(*w.shape[:2], *t.shape[1:]) for t in q))
         return cls(fp8(w13), fp8(w2), **kw)
@@ -261,6 +276,11 @@ class ExpertsLayer:
         `out_dtype` (x's type by default, bf16 for FP8Rows).  A layer in 8 bits takes x as
         FP8Rows with its kind of scales, or quantises it.  The experts' rows stay in fp32
         up to the combine, as in moe."""
+        rows = x[0] if isinstance(x, tuple) and x else x
+        _need(isinstance(rows, torch.Tensor) and rows.dim() == 2, "x must be a [tokens, hidden] tensor or an FP8Rows")
+        # (an index past x's rows would leave rows unwritten, an expert past the weights out)
+        _need(isinstance(logits, torch.Tensor) and logits.shape == (rows.shape[0], self.num_experts),
+              f"logits must be an fp32 [{rows.shape[0]}, {self.num_experts}] tensor")
         if out_dtype is None:
             out_dtype = x.dtype if isinstance(x, torch.Tensor) else torch.bfloat16
         if self.scales is not None and isinstance(x, torch.Tensor):
