@@ -18,14 +18,16 @@
 // the matrix units: w is written out in 16 bits once and the linear operator's tiles
 // multiply it.
 #include "internal.h"
+#include "linear4_map.h"
 #include "linear_kernels.h"
 
 namespace nvfp4 {
 namespace {
 
+using namespace linear4_map;
+
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 // Eight elements as 16-bit numbers: a word of codes times the block scale in byte kByte
 // of `scales`.
@@ -286,9 +288,8 @@ __global__ __launch_bounds__(512) void linear4_few_kernel(const LinParams p) {
 template <int kFM, int kWaves>
 struct TileOf {
   static constexpr int kBM = 16 * kFM, kRowsW = 32 * kWaves, kThreads = 64 * kWaves;
-  static constexpr int kABytes = kBM * 256, kStage = kABytes + kRowsW * 64;
-  static constexpr int kLoadsA = kABytes / (1024 * kWaves), kLoads = kLoadsA + 2;  // 1 KiB copies of a wavefront and step
-  static constexpr int kStages = kFM == 1 ? 5 : kFM == 2 ? 4 : 3;
+  static constexpr int kABytes = tile4_a_bytes(kFM), kStage = tile4_stage(kFM, kWaves), kStages = tile4_stages(kFM);
+  static constexpr int kLoadsA = tile4_loads_a(kFM, kWaves), kLoads = kLoadsA + 2;  // 1 KiB copies of a wavefront and step
 };
 
 template <bool kMx, bool kHalf, int kFM, int kWaves, bool kGated>
@@ -309,30 +310,25 @@ __global__ __launch_bounds__(64 * kWaves, 2) void linear4_tile_kernel(const LinP
   const int64_t m0 = (int64_t)work.tm * kBM;
   const int32_t n0 = work.tn * kOutN;
 
-  // Copies.  a: four rows a copy, 16 chunks of 16 bytes each, chunk c of row r at c ^ (r &
-  // 15); w: 16 rows a copy, four chunks each, at c ^ (r >> 1 & 3).  Rows past the edge
-  // repeat the last one.
+  // copies into LDS: where each lane's come from
   const char* from_a[Tile::kLoadsA];
   const char* from_w[2];
-  const int chunk_w = (lane & 3) ^ (lane >> 3 & 3);
+  const int chunk_w = w_copy4(wave, lane, 0).chunk;            // (the same in both)
 #pragma unroll
   for (int i = 0; i < Tile::kLoadsA; ++i) {
-    const int r = 4 * (wave * Tile::kLoadsA + i) + (lane >> 4);
-    from_a[i] = p.a + min(m0 + r, (int64_t)p.M - 1) * p.lda + ((lane & 15) ^ (r & 15)) * 16 + (int64_t)step0 * 256;
+    const Copy4 c = a_copy4(wave, lane, i, Tile::kLoadsA);
+    from_a[i] = p.a + a_row4(m0, c.row, p.M) * p.lda + c.chunk * 16 + (int64_t)step0 * 256;
   }
-  // (row of the tile -> row of w)
-  auto w_row = [&](int r) { return (int64_t)min(n0 + r % kOutN, p.N - 1) + (r >= kOutN ? p.N : 0); };
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    from_w[i] = p.w + w_row(16 * (2 * wave + i) + (lane >> 2)) * p.ldw + chunk_w * 16 + (int64_t)step0 * 64;
+    from_w[i] = p.w + w_row4(n0, w_copy4(wave, lane, i).row, p.N, kOutN) * p.ldw + chunk_w * 16 + (int64_t)step0 * 64;
   auto fetch = [&](int ks) {
     char* to = smem + ks % kStages * Tile::kStage;
     const int32_t left = K - (step0 + ks) * 128;               // elements of the rows from this step on
 #pragma unroll
     for (int i = 0; i < Tile::kLoadsA; ++i) {
-      const int r = 4 * (wave * Tile::kLoadsA + i) + (lane >> 4), chunk = (lane & 15) ^ (r & 15);
       char* dst = to + (wave * Tile::kLoadsA + i) * 1024;
-      if (chunk * 8 < left) copy_lds16(reinterpret_cast<uint64_t>(from_a[i]), lds_address(dst));
+      if (a_copy4(wave, lane, i, Tile::kLoadsA).chunk * 8 < left) copy_lds16(reinterpret_cast<uint64_t>(from_a[i]), lds_address(dst));
       else *reinterpret_cast<u32x4*>(dst + lane * 16) = u32x4{0, 0, 0, 0};
       from_a[i] += 256;
     }
@@ -348,7 +344,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void linear4_tile_kernel(const LinP
   // scales: two threads a row, two steps each
   const int scale_of = threadIdx.x >> 1, half = threadIdx.x & 1;
   const int32_t nblk = K / (kMx ? 32 : 16);
-  const uint8_t* scale_row = static_cast<const uint8_t*>(p.w_scales) + w_row(scale_of) * nblk;
+  const uint8_t* scale_row = static_cast<const uint8_t*>(p.w_scales) + w_row4(n0, scale_of, p.N, kOutN) * nblk;
   struct Scales {
     uint32_t d[kBlocks / 2];
   };
@@ -517,89 +513,6 @@ __global__ __launch_bounds__(256) void split_rows_kernel(const uint16_t* a, int6
 }
 
 // ---- launches --------------------------------------------------------------------------
-// Which form: fp16 against UE8M0 scales, whose split costs too much in every workgroup,
-// takes the first up to 64 rows and the last beyond.
-struct Plan4 {
-  enum { kFew, kTile, kWide } form;
-  int32_t fm, bm, rows_w, tiles_m, tiles_n, whole, parts, part_steps;
-  size_t bytes;
-  float cost;
-};
-
-// Tiles that fill whole rounds of the CUs are computed whole, those of the last round cut
-// along K, as the linear operator's (plan_of).
-Plan4 tile4_plan(const Linear4Args& a, int fm, int waves, int32_t slots, float step, float rest) {
-  Plan4 q = {};
-  q.form = Plan4::kTile;
-  q.fm = fm;
-  q.bm = 16 * fm;
-  q.rows_w = 32 * waves;
-  q.tiles_m = (a.M - 1) / q.bm + 1;
-  q.tiles_n = (a.N - 1) / (a.gated ? q.rows_w / 2 : q.rows_w) + 1;
-  const int32_t steps = (a.K + 127) / 128;
-  const int64_t total = (int64_t)q.tiles_m * q.tiles_n;
-  if (total > 0x7FFFFFFF / (64 * waves)) {                     // (threads of a launch; the largest tiles always fit)
-    q.cost = 3e38f;
-    return q;
-  }
-  const int32_t left = (int32_t)(total % slots);
-  const float rounds = (float)(total / slots) * (steps * step + rest);
-  for (int32_t parts = 1; parts <= (left ? (slots / left < 16 ? slots / left : 16) : 1); ++parts) {
-    const int32_t each = parts == 1 ? steps : ((steps + parts - 1) / parts + 3) / 4 * 4;  // (scales come in fours)
-    if ((steps + each - 1) / each != parts) continue;
-    float cost = rounds;
-    if (left) cost += each * step + rest;
-    if (parts > 1) cost += 3.0f + (float)left * parts * q.bm * q.rows_w * 8.0f / 8e6f;
-    if (q.cost == 0 || cost < q.cost) {
-      q.cost = cost;
-      q.parts = parts;
-      q.part_steps = each;
-      q.whole = (int32_t)(parts > 1 ? total - left : total);
-      q.bytes = parts > 1 ? (size_t)left * parts * q.bm * q.rows_w * 4 : 0;
-    }
-  }
-  return q;
-}
-
-// Forms' costs in us, by measured rates, and the least of them.  Few rows: w at 3 MB/us,
-// and a again for every 16 rows of w at 14 MB/us from L2.  Tiles of 16, 32, 64 and 128 rows:
-// a step is bound by widening w (E4M3 to bf16 16 instructions for 8 elements of a lane, to
-// fp16 8, UE8M0 4).  Written out: 2.5 bytes an element at 5.3 MB/us, then the linear
-// operator.  Forms measured against each other, in us, at 8192 x 8192 with E4M3 scales in
-// bf16 (few, tiles of 16, 32, 64, 128, written out): 1 row 17, 19, 22, 29, 47, 71; 16 rows
-// 26, 20, 21, 28, 47, 81; 64 rows -, 38, 27, 28, 46, 80; 256 rows -, 119, 66, 58, 51, 118;
-// 1024 rows -, 448, 245, 184, 141, 174.  4096 x (2 x 2112) x 2816: 64-row tiles 142, 128-row
-// tiles 130, written out 114.
-// Sums of parts pass at 8 MB/us (written and read once, mostly in the last-level cache).  At
-// half that rate and 7 us beside the steps of the 16- and 32-row tiles, against 8 and 4:
-// 8192 x 8192 in bf16 58.4 and 51.9 for 256 rows, 96.0 and 84.4 for 512; 512 x (2 x 2112) x
-// 2816 34.7 and 33.2; 16 rows with UE8M0 16.4 and 15.6; but 256 x 1411 x 2112 with UE8M0
-// 12.0 and 14.2, 512 x 1411 x 2112 20.2 and 21.2, 300 x 8192 x 8192 with UE8M0 69.6 and 71.4.
-Plan4 plan4_of(const Linear4Args& a) {
-  Plan4 few = {}, wide = {};
-  few.form = Plan4::kFew;
-  wide.form = Plan4::kWide;
-  if (a.mx && a.kind == kF16) return a.M <= 64 ? few : wide;
-  const float rows = a.gated ? 2.0f * a.N : (float)a.N, weights = rows * a.K;
-  const int c = a.mx ? 2 : a.kind == kF16 ? 1 : 0;
-  static const float kStepUs[4][3] = {{0.9f, 0.76f, 0.58f}, {0.95f, 0.8f, 0.74f}, {1.38f, 1.27f, 1.08f}, {2.1f, 2.0f, 1.87f}};
-  Plan4 best = tile4_plan(a, 1, 4, 512, kStepUs[0][c], 4.0f);
-  auto take = [&](const Plan4& q) {
-    if (q.cost < best.cost) best = q;
-  };
-  if (a.M > 16) take(tile4_plan(a, 2, 4, 512, kStepUs[1][c], 4.0f));
-  if (a.M > 32) take(tile4_plan(a, 4, 4, 512, kStepUs[2][c], 6.0f));
-  if (a.M > 64) take(tile4_plan(a, 8, 8, 256, kStepUs[3][c], 10.0f));
-  if (a.M <= 16) {
-    few.cost = 4.0f + weights * 0.5625f / 3e6f + weights / 16 * a.M * 2 / 14e6f;
-    take(few);
-  } else {
-    wide.cost = 6.0f + weights * 2.5f / 5.3e6f + plan_of(a.M, a.N, 2 * a.K, a.kind, a.gated != 0).cost;
-    take(wide);
-  }
-  return best;
-}
-
 template <bool kMx, bool kHalf, int kRF, int kFN, bool kGated>
 hipError_t go_few(LinParams p, hipStream_t stream) {
   const int32_t cols = kGated ? 8 * kFN : 16 * kFN;
@@ -681,7 +594,7 @@ Wide wide_of(const Linear4Args& a) {
 
 size_t linear4_workspace_bytes(const Linear4Args& a) {
   if (a.M == 0 || a.N == 0) return 0;
-  const Plan4 plan = plan4_of(a);
+  const Plan4 plan = plan4_of(a.M, a.N, a.K, a.kind, a.mx, a.gated != 0);
   if (plan.form != Plan4::kWide) return plan.bytes;
   const Wide q = wide_of(a);
   return q.rest_at + linear_workspace_bytes(q.a);
@@ -690,7 +603,7 @@ size_t linear4_workspace_bytes(const Linear4Args& a) {
 hipError_t launch_linear4(const Linear4Args& a, void* workspace, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const bool f16 = a.kind == kF16;
-  const Plan4 plan = plan4_of(a);
+  const Plan4 plan = plan4_of(a.M, a.N, a.K, a.kind, a.mx, a.gated != 0);
   if (plan.form != Plan4::kWide) {
     LinParams p = {};
     p.a = static_cast<const char*>(a.a);
