@@ -271,9 +271,13 @@ template <int kKind, bool kGated, int kLen>
 struct Columns {
   float b[kLen], bu[kGated ? kLen : 1];
   Scale s[is_row8(kKind) ? kLen : 1], su[is_row8(kKind) && kGated ? kLen : 1];
+  float gain;
 
   __device__ __forceinline__ void load(const LinParams& p, int32_t n) {
     const int have = p.N - n;
+    gain = 1.0f;
+    if constexpr (kKind == kBf16 || kKind == kF16)
+      if (p.gain) gain = *p.gain;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) b[i] = 0.0f;
     if constexpr (kGated) {
@@ -302,17 +306,10 @@ struct Columns {
   __device__ __forceinline__ void finish(const LinParams& p, int64_t m, float* gate, const float* up) const {
     Scale am;
     if constexpr (is_row8(kKind)) am.set(static_cast<const float*>(p.a_scales)[m]);
-    float gain = 1.0f;
-    if constexpr (kKind == kBf16 || kKind == kF16) {
-      if (p.gain) {
-        gain = *p.gain;
-#pragma unroll
-        for (int i = 0; i < kLen; ++i) gate[i] *= gain;
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
       if constexpr (is_row8(kKind)) gate[i] = times_scales(gate[i], am, s[i]);
+      else if constexpr (kKind == kBf16 || kKind == kF16) gate[i] *= gain;
       gate[i] += b[i];
     }
     activate_run<kLen>(gate, p.act);
