@@ -97,8 +97,9 @@ inline Plan4 tile4_plan(int32_t M, int32_t N, int32_t K, bool gated, int fm, int
 // 26, 20, 21, 28, 47, 81; 64 rows -, 38, 27, 28, 46, 80; 256 rows -, 119, 66, 58, 51, 118;
 // 1024 rows -, 448, 245, 184, 141, 174.  4096 x (2 x 2112) x 2816: 64-row tiles 142, 128-row
 // tiles 130, written out 114.
-// Sums of parts pass at 8 MB/us (written and read once, mostly in the last-level cache).  At
-// half that rate and 7 us beside the steps of the 16- and 32-row tiles, against 8 and 4:
+// Sums of parts pass at 8 MB/us (written and read once, mostly in the last-level cache;
+// plan_of's choices are measured with half that rate).  With half that rate here as well,
+// and 7 us beside the steps of the 16- and 32-row tiles, against 8 and 4:
 // 8192 x 8192 in bf16 58.4 and 51.9 for 256 rows, 96.0 and 84.4 for 512; 512 x (2 x 2112) x
 // 2816 34.7 and 33.2; 16 rows with UE8M0 16.4 and 15.6; but 256 x 1411 x 2112 with UE8M0
 // 12.0 and 14.2, 512 x 1411 x 2112 20.2 and 21.2, 300 x 8192 x 8192 with UE8M0 69.6 and 71.4.
