@@ -1,6 +1,6 @@
 // Choice of form, work split and address arithmetic of the linear operator with weights
 // in 4 bits (linear4.hip).  The kernels form their tiles' copies and scales through these
-// functions, and a host-side checker (tests/host/linear4_ranges.cpp) runs the same
+// functions, and a host-side test (tests/host/linear4_ranges.cpp) runs the same
 // functions over the workgroups of a launch: each tile and each of its steps is computed
 // once, and every access lies inside its buffer.  Plain integer arithmetic, no HIP types.
 #pragma once

@@ -61,7 +61,7 @@ int main(int argc, char** argv) {
   const int32_t ms[] = {1, 16, 17, 127, 128, 1000, 4096, 40000, 1 << 20, 1 << 27, (1 << 29) - 1, 1 << 29};
   const int32_t es[] = {1, 2, 63, 64, 65, 128, 1000, 1024};
   const int32_t ns[] = {1, 32, 63, 64, 65, 704, 1411, 8192, 1 << 18, (1 << 24) - 1, 1 << 24};
-  const int32_t ks[] = {16, 128, 24 * kStep, 24 * kStep + 16, 5632, 1 << 23};
+  const int32_t ks[] = {16, 128, 24 * kStep - 16, 24 * kStep + 16, 5632, 1 << 23};
   for (int32_t M : ms)
     for (int32_t E : es)
       for (int32_t N : ns)

@@ -15,7 +15,7 @@ pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 
 
 @pytest.fixture(scope="module")
-def checker(tmp_path_factory):
+def program(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("grouped") / "grouped_limits")
     cmd = ["g++", "-std=c++17", "-O2", "-g", "-fsanitize=address,undefined",
            "-fno-sanitize-recover=all", "-I" + ROOT,
@@ -32,17 +32,17 @@ def run(*cmd, text=None):
     return r.stdout
 
 
-def test_limits(checker):
-    assert "grouped limits ok" in run(checker)
+def test_limits(program):
+    assert "grouped limits ok" in run(program)
 
 
-def test_the_gpu_tests_reach_every_tile(checker):
+def test_the_gpu_tests_reach_every_tile(program):
     cases, lines = list(C.all_cases()), ""
     for kind, tile, K, gated, _ in cases:
         sizes, N, Ng = C.TILES[tile]
         code = ["bf16", "fp16", "row", "mx"].index(kind)
         lines += f"{sum(sizes)} {len(sizes)} {Ng if gated else N} {K * (2 if code < 2 else 1)} {code} {int(gated)}\n"
-    for case, tile in zip(cases, run(checker, "plan", text=lines).split()):
+    for case, tile in zip(cases, run(program, "plan", text=lines).split()):
         assert int(tile) == case[1], f"{case}: the plan takes tiles of {tile} rows"
     for tile, (sizes, _, _) in C.TILES.items():
         last = {(n - 1) % tile + 1 for n in sizes if n}

@@ -15,7 +15,7 @@ pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 
 
 @pytest.fixture(scope="module")
-def checker(tmp_path_factory):
+def program(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("linear4") / "linear4_ranges")
     cmd = ["g++", "-std=c++17", "-O2", "-g", "-fsanitize=address,undefined",
            "-fno-sanitize-recover=all", "-I" + ROOT,
@@ -32,15 +32,15 @@ def run(*cmd, text=None):
     return r.stdout
 
 
-def test_work_split_and_addresses(checker):
-    assert "linear4 ranges ok" in run(checker)
+def test_work_split_and_addresses(program):
+    assert "linear4 ranges ok" in run(program)
 
 
-def test_the_gpu_tests_reach_every_kernel(checker):
+def test_the_gpu_tests_reach_every_kernel(program):
     cases = list(C.all_cases())
     lines = "".join(f"{M} {N} {K} {int(dtype == 'fp16')} {int(scales == 'mx')} {int(gated)}\n"
                     for scales, dtype, _, _, _, M, N, K, gated in cases)
-    plans = run(checker, "plan", text=lines).splitlines()
+    plans = run(program, "plan", text=lines).splitlines()
     assert len(plans) == len(cases)
     seen = set()
     for c, line in zip(cases, plans):
